@@ -22,6 +22,13 @@
  * tree_attention_paged and kv_commit_paged are the two cache calls over a
  * paged KV cache (a page pool and a block table).
  *
+ * Before and between such steps, the paged cache is filled and read by
+ *   kv_page_plan           block tables and slot maps from request lengths
+ *   kv_append_paged        K/V rows of new tokens to their slots
+ *   prompt_attention       causal attention over packed whole prompts
+ *   chunk_attention_paged  causal attention of chunks of new tokens (one:
+ *                          plain decoding) over the paged cache
+ *
  * Sources of the operations (public web pages on Medusa):
  *   [SPEC]  "Speculative Decoding & Medusa Tree Attention: Accelerating LLM
  *           Inference by 3x Without Accuracy Loss", section 2 "The
@@ -81,7 +88,9 @@ enum {
     MEDUSA_STATUS_TIMEOUT = 16,       /* an internal pipeline wait gave up after ~2 s (a library bug), or after
                                          the limit set by medusa_debug_set_wait_limit */
     MEDUSA_STATUS_BAD_PAGE = 32,      /* a needed block-table entry outside [0, num_pages) */
-    MEDUSA_STATUS_BAD_LAYER = 64      /* kv_compact: a layer's cache pointer is NULL or not 16-byte aligned */
+    MEDUSA_STATUS_BAD_LAYER = 64,     /* kv_compact: a layer's cache pointer is NULL or not 16-byte aligned */
+    MEDUSA_STATUS_BAD_LENGTH = 128    /* a count or row start outside its range (kv_page_plan, prompt_attention,
+                                         chunk_attention_paged) */
 };
 
 typedef enum { MEDUSA_F32 = 0, MEDUSA_BF16 = 1 } medusa_dtype;
@@ -570,6 +579,139 @@ int kv_commit_paged(void* k_pages, void* v_pages, const void* k_tree, const void
                     int max_pages, int page_size, int num_pages, const int32_t* accept_path, int max_path,
                     const int32_t* accept_len, const int32_t* prefix_len, int32_t* new_prefix_len, int B, int T,
                     int Hkv, int D, medusa_dtype dt, int32_t* status, medusa_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Prompts and single tokens over the paged cache                            */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The tree step starts from a cache that holds every sequence's prefix.  The
+ * four calls below bring the prefixes there ([MTP] "Production Deployment
+ * Guidelines" names PagedAttention; the pages describe no prompt phase, so
+ * these are library conveniences, not steps of the method).  They work on
+ * packed batches: the new tokens of sequence b are rows
+ *     [row_start[b], row_start[b + 1])        row_start [B + 1] int32, device
+ * of arrays of N rows, at positions prefix_len[b], prefix_len[b] + 1, ...
+ * Rows at or past row_start[B] belong to no sequence: they are not read and
+ * their outputs are left as they were (a captured call may be replayed with
+ * fewer tokens than it was captured with).  A sequence may have no new token.
+ * A contiguous cache [B, Hkv, S_max, D] is the pool of B pages of S_max rows
+ * with block_table[b] = b (max_pages = 1).
+ */
+
+/*
+ * One scheduler step of a page pool: takes pages from the free stack for the
+ * sequences that grow, takes back the pages of those that ended, and maps
+ * every new token to its slot, in one launch.
+ *   new_len[b] >= 0: the sequence needs the pages of its first
+ *     want = ceil((prefix_len[b] + new_len[b] + room) / page_size)
+ *     blocks (room >= 0 rows more than its new tokens: a tree step's commit,
+ *     say).  With owned[b] < want, entries owned[b] .. want - 1 of its table
+ *     row are taken from the top of the stack, sequences in index order,
+ *     blocks in order; it never gives pages back.
+ *   new_len[b] = -1: the sequence has ended; its owned[b] pages are pushed on
+ *     the stack (sequences in index order, blocks in order) before any page
+ *     is taken.
+ *
+ * prefix_len [B], new_len [B] int32
+ * block_table [B, max_pages] int32, in place (only taken entries are written;
+ *   the entries of an ended sequence keep their values)
+ * owned [B] in, owned_out [B] out (may be the same array)
+ * free_list [num_pages] int32: a stack of the pages nobody owns, entries
+ *   [0, free_count); only entries of pushed pages are written (at and past
+ *   free_count)
+ * free_count [1] in, free_count_out [1] out (may be the same word)
+ * row_start [B + 1] int32 out: the prefix sum of max(new_len, 0)
+ * slot_map [max_tokens] int64 out: page * page_size + row within the page of
+ *   each packed new token; -1 for tokens of a sequence that got no pages and
+ *   for rows at or past row_start[B]
+ * A sequence is served when its pages and those of all sequences before it
+ * fit the stack; one that is not (or that needs more than max_pages blocks)
+ * keeps its table row and owned count, its tokens' slots are -1, and
+ * MEDUSA_STATUS_CACHE_OVERFLOW is set.  new_len < -1 (taken as 0), owned or
+ * free_count out of range (clamped) and more than max_tokens new tokens (row
+ * starts clamped to max_tokens) set MEDUSA_STATUS_BAD_LENGTH, a negative
+ * prefix_len (not served) MEDUSA_STATUS_BAD_PREFIX, a page outside
+ * [0, num_pages) on the stack or in a table MEDUSA_STATUS_BAD_PAGE (its
+ * entry and slots become -1).
+ * The calls that use one pool are ordered by the caller: two plans on the
+ * same state may not overlap.
+ * Limits: B <= 8192; max_tokens >= 1.
+ */
+int kv_page_plan(const int32_t* prefix_len, const int32_t* new_len, int B, int room, int32_t* block_table,
+                 int max_pages, int page_size, int num_pages, const int32_t* owned, int32_t* owned_out,
+                 int32_t* free_list, const int32_t* free_count, int32_t* free_count_out, int32_t* row_start,
+                 int64_t* slot_map, int max_tokens, int32_t* status, medusa_stream_t stream);
+
+/*
+ * Writes the K/V of N packed new tokens to their slots, bit for bit:
+ *     pages[slot_map[t] / page_size, g, slot_map[t] % page_size, :] = rows[t, g, :]
+ * k, v: rows of Hkv * D contiguous elements, k_stride and v_stride elements
+ *   apart (>= Hkv * D and a multiple of 16 bytes: views into a fused
+ *   projection's rows are taken as they are)
+ * slot_map [N] int64: slots, distinct; -1 skips the row.  Other values
+ *   outside [0, num_pages * page_size) are skipped too and set
+ *   MEDUSA_STATUS_BAD_PAGE.
+ * Limits: D in {64, 128}; N >= 0.
+ */
+int kv_append_paged(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int64_t* slot_map, int N,
+                    void* k_pages, void* v_pages, int page_size, int num_pages, int Hkv, int D, medusa_dtype dt,
+                    int32_t* status, medusa_stream_t stream);
+
+/*
+ * Causal attention of packed whole prompts over their own K/V (nothing
+ * cached): for token i of a sequence and query head h (kv-head g = h / (Hq /
+ * Hkv)),
+ *     O[i,h,:] = sum_{j <= i} softmax_j(scale * <q[i,h,:], k[j,g,:]>) v[j,g,:]
+ * q [N, Hq, D], k, v [N, Hkv, D] dtype dt, tokens q_stride, k_stride,
+ *   v_stride elements apart (multiples of 16 bytes; heads contiguous)
+ * max_len: an upper bound of the sequences' lengths (0: N).  A longer one, or
+ *   row starts that fall or leave [0, N], set MEDUSA_STATUS_BAD_LENGTH; the
+ *   rows past the bound are not computed.
+ * scale: softmax scale; <= 0 means 1/sqrt(D)
+ * out [N, Hq, D] dtype dt (contiguous); lse [N, Hq] f32, nullable: natural
+ *   log-sum-exp of the scaled scores
+ * K/V of tokens that a row does not see never reach its output, whatever
+ * they hold (NaN and infinities included).
+ * fp32 computes in fp32 throughout; bf16 multiplies bf16 weights (fp32
+ * statistics and sums) and rounds once at the end.
+ * Limits: D in {64, 128}; Hq % Hkv == 0 and Hq / Hkv <= 64.
+ * Workspace: prompt_attention_workspace_size(...) bytes; calls that may
+ * overlap (other streams, graphs replayed side by side) need separate ones.
+ */
+size_t prompt_attention_workspace_size(int B, int N, int max_len, int Hq, int Hkv, int D, medusa_dtype dt);
+int prompt_attention(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                     int64_t v_stride, const int32_t* row_start, int B, int N, int max_len, int Hq, int Hkv, int D,
+                     float scale, medusa_dtype dt, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                     int32_t* status, medusa_stream_t stream);
+
+/*
+ * Causal attention of chunks of new tokens over the paged cache, which
+ * already holds the chunks' own K/V (kv_append_paged): token i of sequence b
+ * attends to positions 0 .. prefix_len[b] + i, read through the block table.
+ * One token per sequence is plain decoding.  q, row_start, scale, out, lse
+ * and the formats as prompt_attention; k_pages, v_pages, block_table as
+ * tree_attention_paged.
+ * max_new: an upper bound of the chunks' lengths (0: N); max_prefix: of the
+ *   prefix lengths (0: max_pages * page_size).  Both size the launch: a tight
+ *   bound is faster.  A longer chunk, or one past the table's last page, sets
+ *   MEDUSA_STATUS_BAD_LENGTH (the rows past the bound are not computed); a
+ *   prefix outside [0, max_prefix] sets MEDUSA_STATUS_BAD_PREFIX and is
+ *   clamped.  A needed table entry outside [0, num_pages) sets
+ *   MEDUSA_STATUS_BAD_PAGE; that sequence's output is then not meaningful.
+ * Slots at or past the last new token may hold anything.
+ * Limits as prompt_attention; any page_size >= 1 (bf16: the tensor-core
+ * kernels read sizes of 8, 16, 32 and multiples of 64; others run on CUDA
+ * cores).
+ * Workspace: chunk_attention_paged_workspace_size(...) bytes.
+ */
+size_t chunk_attention_paged_workspace_size(int B, int N, int max_new, int max_prefix, int max_pages, int page_size,
+                                            int Hq, int Hkv, int D, medusa_dtype dt);
+int chunk_attention_paged(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages,
+                          const int32_t* block_table, int max_pages, int page_size, int num_pages,
+                          const int32_t* row_start, const int32_t* prefix_len, int B, int N, int max_new,
+                          int max_prefix, int Hq, int Hkv, int D, float scale, medusa_dtype dt, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, int32_t* status, medusa_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -419,3 +419,262 @@ class MedusaStep:
             return
         self.verify(target, q_draft, q_row, seed, step, node_tokens)
         self.commit(k_cache, v_cache, k_tree, v_tree, prefix_len, new_prefix_len, block_table, k_layers, v_layers)
+
+
+# ----------------------------------------------------------------------------
+# prompts and single tokens over the paged cache
+# ----------------------------------------------------------------------------
+
+def _need(ok: bool, msg: str) -> None:
+    if not ok:
+        raise ValueError(msg)
+
+
+def _ints(name: str, t: torch.Tensor, shape, device, dtype=torch.int32) -> None:
+    """An index array: dtype, device, shape (None: any extent), contiguous."""
+    _need(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
+    _need(t.device == device, f"{name} is on {t.device}, expected {device}")
+    _need(t.dim() == len(shape) and all(w is None or w == n for w, n in zip(shape, t.shape)),
+          f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    _need(t.is_contiguous(), f"{name} must be contiguous")
+
+
+def _rows(name: str, t: torch.Tensor, N, heads: int, D: int, dtype, device) -> int:
+    """Packed rows [N, heads, D]: a row's heads contiguous, rows any (16-byte
+    multiple) stride apart.  Returns the row stride in elements."""
+    _need(t.dim() == 3 and (N is None or t.shape[0] == N) and t.shape[1] == heads and t.shape[2] == D,
+          f"{name} must have shape {[N, heads, D]}, got {list(t.shape)}")
+    _need(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
+    _need(t.device == device, f"{name} is on {t.device}, expected {device}")
+    s = t.stride()
+    _need(t.numel() == 0 or ((s[2] == 1 or D == 1) and (s[1] == D or heads == 1)),
+          f"{name}: the heads of a row must be contiguous, got strides {s}")
+    return s[0] if t.shape[0] > 1 else heads * D
+
+
+def _pool(name: str, t: torch.Tensor, dtype, device) -> None:
+    _need(t.dim() == 4 and t.is_contiguous(), f"{name} must be a contiguous [num_pages, Hkv, page_size, D] pool")
+    _need(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
+    _need(t.device == device, f"{name} is on {t.device}, expected {device}")
+
+
+def kv_page_plan(prefix_len, new_len, block_table, owned, free_list, free_count, page_size: int, max_tokens: int,
+                 room: int = 0) -> Dict[str, torch.Tensor]:
+    """One step of a page pool: pages for the sequences that grow (new_len[b]
+    new tokens and ``room`` more rows), the pages of ended ones (new_len[b] =
+    -1) back on the free stack, and a slot for every packed new token.
+    ``block_table`` [B,max_pages] and ``free_list`` [num_pages] are updated in
+    place; the new ``owned`` [B], ``free_count`` [1], ``row_start`` [B+1] and
+    ``slot_map`` [max_tokens] int64 are returned."""
+    B, dev = prefix_len.shape[0], prefix_len.device
+    _ints("prefix_len", prefix_len, (B,), dev)
+    _ints("new_len", new_len, (B,), dev)
+    _ints("block_table", block_table, (B, None), dev)
+    _ints("owned", owned, (B,), dev)
+    _ints("free_list", free_list, (None,), dev)
+    _ints("free_count", free_count, (1,), dev)
+    out = {
+        "row_start": torch.empty((B + 1,), dtype=torch.int32, device=dev),
+        "slot_map": torch.empty((max(max_tokens, 0),), dtype=torch.int64, device=dev),
+        "owned": torch.empty_like(owned),
+        "free_count": torch.empty_like(free_count),
+        "status": _status(dev),
+    }
+    with torch.cuda.device(dev):
+        _b.kv_page_plan(prefix_len, new_len, B, room, block_table, block_table.shape[1], page_size,
+                        free_list.shape[0], owned, out["owned"], free_list, free_count, out["free_count"],
+                        out["row_start"], out["slot_map"], max_tokens, out["status"])
+    return out
+
+
+def kv_append_paged(k, v, slot_map, k_pages, v_pages) -> Dict[str, torch.Tensor]:
+    """Writes packed K/V rows [N,Hkv,D] (views with any row stride) to their
+    slots of the pools [num_pages,Hkv,page_size,D], in place; slot -1 skips a
+    row.  ``slot_map`` has at least N entries."""
+    dev, dt = k_pages.device, k_pages.dtype
+    _pool("k_pages", k_pages, dt, dev)
+    _pool("v_pages", v_pages, dt, dev)
+    _need(k_pages.shape == v_pages.shape, "k_pages and v_pages must have the same shape")
+    num_pages, Hkv, page_size, D = k_pages.shape
+    N = k.shape[0]
+    ks = _rows("k", k, N, Hkv, D, dt, dev)
+    vs = _rows("v", v, N, Hkv, D, dt, dev)
+    _ints("slot_map", slot_map, (None,), dev, torch.int64)
+    _need(slot_map.shape[0] >= N, f"slot_map has {slot_map.shape[0]} entries for {N} rows")
+    st = _status(dev)
+    with torch.cuda.device(dev):
+        _b.kv_append_paged(k, v, ks, vs, slot_map, N, k_pages, v_pages, page_size, num_pages, Hkv, D,
+                           _b.dtype_code(dt), st)
+    return {"status": st}
+
+
+def prompt_attention(q, k, v, row_start, scale: float = 0.0, max_len: int = 0,
+                     want_lse: bool = False) -> Dict[str, torch.Tensor]:
+    """Causal attention of packed whole prompts: q [N,Hq,D], k, v [N,Hkv,D]
+    (views with any row stride), sequence b = rows row_start[b] ..
+    row_start[b+1].  ``max_len`` bounds the lengths (0: N).  Rows of no
+    sequence are zero in the returned output (lse 0)."""
+    N, Hq, D = q.shape
+    Hkv, dev, dt = k.shape[1], q.device, q.dtype
+    qs = _rows("q", q, N, Hq, D, dt, dev)
+    ks = _rows("k", k, N, Hkv, D, dt, dev)
+    vs = _rows("v", v, N, Hkv, D, dt, dev)
+    _ints("row_start", row_start, (None,), dev)
+    B = row_start.shape[0] - 1
+    out = {"out": torch.zeros((N, Hq, D), dtype=dt, device=dev), "status": _status(dev)}
+    if want_lse:
+        out["lse"] = torch.zeros((N, Hq), dtype=torch.float32, device=dev)
+    code = _b.dtype_code(dt)
+    with torch.cuda.device(dev):
+        nb = _b.prompt_attention_workspace_size(B, N, max_len, Hq, Hkv, D, code)
+        _b.prompt_attention(q, k, v, qs, ks, vs, row_start, B, N, max_len, Hq, Hkv, D, scale, code, out["out"],
+                            out.get("lse"), _ws(nb, dev), nb, out["status"])
+    return out
+
+
+def chunk_attention_paged(q, k_pages, v_pages, block_table, row_start, prefix_len, scale: float = 0.0,
+                          max_new: int = 0, max_prefix: int = 0, want_lse: bool = False) -> Dict[str, torch.Tensor]:
+    """Causal attention of packed chunks of new tokens (q [N,Hq,D]; one token
+    per sequence: plain decoding) over the paged cache that already holds
+    their K/V.  ``max_new`` and ``max_prefix`` bound the chunk and prefix
+    lengths (0: N, the table's capacity).  Rows of no sequence are zero in
+    the returned output (lse 0)."""
+    N, Hq, D = q.shape
+    dev, dt = q.device, q.dtype
+    qs = _rows("q", q, N, Hq, D, dt, dev)
+    _pool("k_pages", k_pages, dt, dev)
+    _pool("v_pages", v_pages, dt, dev)
+    _need(k_pages.shape == v_pages.shape and k_pages.shape[3] == D, "k_pages and v_pages must be equal pools of D")
+    num_pages, Hkv, page_size, _ = k_pages.shape
+    B = prefix_len.shape[0]
+    _ints("prefix_len", prefix_len, (B,), dev)
+    _ints("row_start", row_start, (B + 1,), dev)
+    _ints("block_table", block_table, (B, None), dev)
+    mp = block_table.shape[1]
+    out = {"out": torch.zeros((N, Hq, D), dtype=dt, device=dev), "status": _status(dev)}
+    if want_lse:
+        out["lse"] = torch.zeros((N, Hq), dtype=torch.float32, device=dev)
+    code = _b.dtype_code(dt)
+    with torch.cuda.device(dev):
+        nb = _b.chunk_attention_paged_workspace_size(B, N, max_new, max_prefix, mp, page_size, Hq, Hkv, D, code)
+        _b.chunk_attention_paged(q, qs, k_pages, v_pages, block_table, mp, page_size, num_pages, row_start,
+                                 prefix_len, B, N, max_new, max_prefix, Hq, Hkv, D, scale, code, out["out"],
+                                 out.get("lse"), _ws(nb, dev), nb, out["status"])
+    return out
+
+
+class PromptStep:
+    """The buffers of a packed batch of new tokens of a fixed capacity,
+    allocated once: what ``MedusaStep`` is for tree steps, for the prompts
+    and single tokens that fill the cache before and between them.
+
+    ``plan`` takes pages and maps the new tokens to slots (``row_start``,
+    ``slot_map``), ``append`` writes a layer's K/V there, ``chunk_attention``
+    attends over the paged cache and ``prompt_attention`` over packed prompts
+    of which nothing is cached; results are in ``out`` [max_tokens,Hq,D] (and
+    ``lse`` with ``want_lse``).  Each is one asynchronous library call on the
+    current stream without allocation, so a sequence of them can be captured
+    in a CUDA graph and replayed with other lengths, up to ``max_tokens`` new
+    tokens, ``max_new`` of them per sequence (0: max_tokens) and prefixes of
+    ``max_prefix`` (0: the tables' capacity).  ``status`` collects the
+    data-dependent errors of all calls.  One PromptStep serves one stream at
+    a time."""
+
+    def __init__(self, *, B: int, Hq: int, Hkv: int, D: int, max_tokens: int, dtype: torch.dtype, max_new: int = 0,
+                 max_prefix: int = 0, page_size: int = 0, max_pages: int = 0, num_pages: int = 0, room: int = 0,
+                 scale: float = 0.0, want_lse: bool = False, device=None):
+        dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device, self.dtype, self.dt = dev, dtype, _b.dtype_code(dtype)
+        self.B, self.Hq, self.Hkv, self.D = B, Hq, Hkv, D
+        self.max_tokens, self.max_new, self.max_prefix = max_tokens, max_new, max_prefix
+        self.page_size, self.max_pages, self.num_pages = page_size, max_pages, num_pages
+        self.room, self.scale = room, scale
+        self.row_start = torch.zeros((B + 1,), dtype=torch.int32, device=dev)
+        self.slot_map = torch.full((max_tokens,), -1, dtype=torch.int64, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.out = torch.zeros((max_tokens, Hq, D), dtype=dtype, device=dev)
+        self.lse = torch.zeros((max_tokens, Hq), dtype=torch.float32, device=dev) if want_lse else None
+        with torch.cuda.device(dev):
+            n = _b.prompt_attention_workspace_size(B, max_tokens, max_new, Hq, Hkv, D, self.dt)
+            if page_size > 0:
+                n = max(n, _b.chunk_attention_paged_workspace_size(B, max_tokens, max_new, max_prefix, max_pages,
+                                                                   page_size, Hq, Hkv, D, self.dt))
+        self.ws_n = n
+        self.ws = _ws(n, dev)
+
+    def _tokens(self, t: torch.Tensor) -> int:
+        _need(t.shape[0] <= self.max_tokens, f"{t.shape[0]} rows, the step holds {self.max_tokens}")
+        return t.shape[0]
+
+    def _starts(self, row_start) -> torch.Tensor:
+        if row_start is None:
+            return self.row_start
+        _ints("row_start", row_start, (self.B + 1,), self.device)
+        return row_start
+
+    def _pools(self, k_pages, v_pages) -> None:
+        shape = (self.num_pages, self.Hkv, self.page_size, self.D)
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            _pool(name, t, self.dtype, self.device)
+            _need(t.shape == shape, f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+    def plan(self, prefix_len, new_len, block_table, owned, free_list, free_count, owned_out=None,
+             free_count_out=None):
+        """Takes and gives back pages (``owned`` and ``free_count`` in place
+        unless outputs are given) and fills ``row_start`` and ``slot_map``."""
+        dev = self.device
+        owned_out = owned if owned_out is None else owned_out
+        free_count_out = free_count if free_count_out is None else free_count_out
+        for name, t in (("prefix_len", prefix_len), ("new_len", new_len), ("owned", owned), ("owned_out", owned_out)):
+            _ints(name, t, (self.B,), dev)
+        _ints("block_table", block_table, (self.B, self.max_pages), dev)
+        _ints("free_list", free_list, (self.num_pages,), dev)
+        _ints("free_count", free_count, (1,), dev)
+        _ints("free_count_out", free_count_out, (1,), dev)
+        with torch.cuda.device(dev):
+            _b.kv_page_plan(prefix_len, new_len, self.B, self.room, block_table, self.max_pages, self.page_size,
+                            self.num_pages, owned, owned_out, free_list, free_count, free_count_out, self.row_start,
+                            self.slot_map, self.max_tokens, self.status)
+
+    def append(self, k, v, k_pages, v_pages, slot_map=None):
+        """K/V rows [N,Hkv,D] of the packed new tokens to their slots (of the
+        last ``plan``, or ``slot_map``)."""
+        N = self._tokens(k)
+        ks = _rows("k", k, N, self.Hkv, self.D, self.dtype, self.device)
+        vs = _rows("v", v, N, self.Hkv, self.D, self.dtype, self.device)
+        self._pools(k_pages, v_pages)
+        if slot_map is None:
+            slot_map = self.slot_map
+        else:
+            _ints("slot_map", slot_map, (None,), self.device, torch.int64)
+            _need(slot_map.shape[0] >= N, f"slot_map has {slot_map.shape[0]} entries for {N} rows")
+        with torch.cuda.device(self.device):
+            _b.kv_append_paged(k, v, ks, vs, slot_map, N, k_pages, v_pages, self.page_size, self.num_pages, self.Hkv,
+                               self.D, self.dt, self.status)
+
+    def prompt_attention(self, q, k, v, row_start=None):
+        """Packed whole prompts q [N,Hq,D], k, v [N,Hkv,D]."""
+        N = self._tokens(q)
+        qs = _rows("q", q, N, self.Hq, self.D, self.dtype, self.device)
+        ks = _rows("k", k, N, self.Hkv, self.D, self.dtype, self.device)
+        vs = _rows("v", v, N, self.Hkv, self.D, self.dtype, self.device)
+        row_start = self._starts(row_start)
+        with torch.cuda.device(self.device):
+            _b.prompt_attention(q, k, v, qs, ks, vs, row_start, self.B, N, self.max_new, self.Hq, self.Hkv, self.D,
+                                self.scale, self.dt, self.out, self.lse, self.ws, self.ws_n, self.status)
+
+    def chunk_attention(self, q, k_pages, v_pages, block_table, prefix_len, row_start=None):
+        """Packed chunks q [N,Hq,D] over the paged cache."""
+        N = self._tokens(q)
+        qs = _rows("q", q, N, self.Hq, self.D, self.dtype, self.device)
+        self._pools(k_pages, v_pages)
+        _ints("block_table", block_table, (self.B, self.max_pages), self.device)
+        _ints("prefix_len", prefix_len, (self.B,), self.device)
+        row_start = self._starts(row_start)
+        with torch.cuda.device(self.device):
+            _b.chunk_attention_paged(q, qs, k_pages, v_pages, block_table, self.max_pages, self.page_size,
+                                     self.num_pages, row_start, prefix_len, self.B, N, self.max_new, self.max_prefix,
+                                     self.Hq, self.Hkv, self.D, self.scale, self.dt, self.out, self.lse, self.ws,
+                                     self.ws_n, self.status)

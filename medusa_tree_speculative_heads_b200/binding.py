@@ -33,6 +33,7 @@ STATUS_NO_MASS = 8
 STATUS_TIMEOUT = 16
 STATUS_BAD_PAGE = 32
 STATUS_BAD_LAYER = 64
+STATUS_BAD_LENGTH = 128
 
 F32, BF16 = 0, 1
 GREEDY, STOCHASTIC = 0, 1
@@ -104,6 +105,17 @@ def lib() -> ctypes.CDLL:
                                            i32, vp, vp, vp, vp, sz, vp, vp]
         L.kv_commit_paged.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32,
                                       vp, vp]
+        i64 = ctypes.c_int64
+        L.kv_page_plan.argtypes = [vp, vp, i32, i32, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp]
+        L.kv_append_paged.argtypes = [vp, vp, i64, i64, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp]
+        L.prompt_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+        L.prompt_attention_workspace_size.restype = sz
+        L.prompt_attention.argtypes = [vp, vp, vp, i64, i64, i64, vp, i32, i32, i32, i32, i32, i32, f32, i32, vp, vp,
+                                       vp, sz, vp, vp]
+        L.chunk_attention_paged_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32, i32, i32, i32]
+        L.chunk_attention_paged_workspace_size.restype = sz
+        L.chunk_attention_paged.argtypes = [vp, i64, vp, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, i32, i32, i32,
+                                            i32, f32, i32, vp, vp, vp, sz, vp, vp]
         _lib = L
     return _lib
 
@@ -343,3 +355,41 @@ def kv_commit_paged(k_pages, v_pages, k_tree, v_tree, block_table, max_pages, pa
     _check(lib().kv_commit_paged(_p(k_pages), _p(v_pages), _p(k_tree), _p(v_tree), _p(block_table), max_pages,
                                  page_size, num_pages, _p(accept_path), max_path, _p(accept_len), _p(prefix_len),
                                  _p(new_prefix_len), B, T, Hkv, D, dt, _p(status), _stream(stream)))
+
+
+def kv_page_plan(prefix_len, new_len, B, room, block_table, max_pages, page_size, num_pages, owned, owned_out,
+                 free_list, free_count, free_count_out, row_start, slot_map, max_tokens, status, stream=None):
+    _check(lib().kv_page_plan(_p(prefix_len), _p(new_len), B, room, _p(block_table), max_pages, page_size, num_pages,
+                              _p(owned), _p(owned_out), _p(free_list), _p(free_count), _p(free_count_out),
+                              _p(row_start), _p(slot_map), max_tokens, _p(status), _stream(stream)))
+
+
+def kv_append_paged(k, v, k_stride, v_stride, slot_map, N, k_pages, v_pages, page_size, num_pages, Hkv, D, dt, status,
+                    stream=None):
+    """Strides in elements between tokens."""
+    _check(lib().kv_append_paged(_p(k), _p(v), k_stride, v_stride, _p(slot_map), N, _p(k_pages), _p(v_pages),
+                                 page_size, num_pages, Hkv, D, dt, _p(status), _stream(stream)))
+
+
+def prompt_attention_workspace_size(B, N, max_len, Hq, Hkv, D, dt) -> int:
+    return lib().prompt_attention_workspace_size(B, N, max_len, Hq, Hkv, D, dt)
+
+
+def prompt_attention(q, k, v, q_stride, k_stride, v_stride, row_start, B, N, max_len, Hq, Hkv, D, scale, dt, out, lse,
+                     workspace, workspace_bytes, status, stream=None):
+    _check(lib().prompt_attention(_p(q), _p(k), _p(v), q_stride, k_stride, v_stride, _p(row_start), B, N, max_len, Hq,
+                                  Hkv, D, float(scale), dt, _p(out), _p(lse), _p(workspace), workspace_bytes,
+                                  _p(status), _stream(stream)))
+
+
+def chunk_attention_paged_workspace_size(B, N, max_new, max_prefix, max_pages, page_size, Hq, Hkv, D, dt) -> int:
+    return lib().chunk_attention_paged_workspace_size(B, N, max_new, max_prefix, max_pages, page_size, Hq, Hkv, D, dt)
+
+
+def chunk_attention_paged(q, q_stride, k_pages, v_pages, block_table, max_pages, page_size, num_pages, row_start,
+                          prefix_len, B, N, max_new, max_prefix, Hq, Hkv, D, scale, dt, out, lse, workspace,
+                          workspace_bytes, status, stream=None):
+    _check(lib().chunk_attention_paged(_p(q), q_stride, _p(k_pages), _p(v_pages), _p(block_table), max_pages,
+                                       page_size, num_pages, _p(row_start), _p(prefix_len), B, N, max_new, max_prefix,
+                                       Hq, Hkv, D, float(scale), dt, _p(out), _p(lse), _p(workspace), workspace_bytes,
+                                       _p(status), _stream(stream)))

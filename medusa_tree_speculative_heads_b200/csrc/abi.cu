@@ -918,3 +918,221 @@ extern "C" int kv_commit_paged(void* k_pages, void* v_pages, const void* k_tree,
     if (e != cudaSuccess) return cuda_fail(e, "kv_commit_paged launch");
     return ok();
 }
+
+// ---------------------------------------------------------------------------
+// prompts and single tokens over the paged cache
+// ---------------------------------------------------------------------------
+
+extern "C" int kv_page_plan(const int32_t* prefix_len, const int32_t* new_len, int B, int room, int32_t* block_table,
+                            int max_pages, int page_size, int num_pages, const int32_t* owned, int32_t* owned_out,
+                            int32_t* free_list, const int32_t* free_count, int32_t* free_count_out,
+                            int32_t* row_start, int64_t* slot_map, int max_tokens, int32_t* status,
+                            medusa_stream_t stream) {
+    if (!prefix_len || !new_len || !block_table || !owned || !owned_out || !free_list || !free_count ||
+        !free_count_out || !row_start || !slot_map)
+        return fail(MEDUSA_ERR_INVALID_ARG, "kv_page_plan: NULL tensor argument");
+    if (B < 1 || room < 0 || max_pages < 1 || page_size < 1 || num_pages < 1 || max_tokens < 1 ||
+        (long)max_pages * page_size > (1L << 30))
+        return fail(MEDUSA_ERR_INVALID_ARG,
+                    "kv_page_plan: bad sizes B=%d room=%d max_pages=%d page_size=%d num_pages=%d max_tokens=%d", B,
+                    room, max_pages, page_size, num_pages, max_tokens);
+    if (B > kMaxPlanSeqs)
+        return fail(MEDUSA_ERR_UNSUPPORTED, "kv_page_plan: B = %d > %d", B, kMaxPlanSeqs);
+    if ((uintptr_t)slot_map & 7u) return fail(MEDUSA_ERR_INVALID_ARG, "kv_page_plan: slot_map must be 8-byte aligned");
+    PagePlanArgs a;
+    a.prefix_len = prefix_len;
+    a.new_len = new_len;
+    a.block_table = block_table;
+    a.owned = owned;
+    a.free_list = free_list;
+    a.free_count = free_count;
+    a.owned_out = owned_out;
+    a.free_count_out = free_count_out;
+    a.row_start = row_start;
+    a.slot_map = slot_map;
+    a.B = B;
+    a.room = room;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.max_tokens = max_tokens;
+    a.status = status;
+    cudaError_t e = page_plan_launch(a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_page_plan launch");
+    return ok();
+}
+
+// a row stride (elements) of tokens of `width` elements that 16-byte accesses
+// can follow
+static bool stride_ok(int64_t stride, long width, int esize) {
+    return stride >= width && stride <= (1L << 31) && stride * esize % 16 == 0;
+}
+
+extern "C" int kv_append_paged(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                               const int64_t* slot_map, int N, void* k_pages, void* v_pages, int page_size,
+                               int num_pages, int Hkv, int D, medusa_dtype dt, int32_t* status,
+                               medusa_stream_t stream) {
+    if (dt != MEDUSA_F32 && dt != MEDUSA_BF16) return fail(MEDUSA_ERR_UNSUPPORTED, "kv_append_paged: unknown dtype");
+    if ((N != 0 && (!k || !v || !slot_map)) || !k_pages || !v_pages)
+        return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_paged: NULL tensor argument");
+    if (N < 0 || page_size < 1 || num_pages < 1 || Hkv < 1 || Hkv > 1024)
+        return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_paged: bad sizes N=%d page_size=%d num_pages=%d Hkv=%d", N,
+                    page_size, num_pages, Hkv);
+    if (D != 64 && D != 128) return fail(MEDUSA_ERR_UNSUPPORTED, "kv_append_paged: head_dim %d (64 or 128)", D);
+    const int esize = dt == MEDUSA_F32 ? 4 : 2;
+    if (!stride_ok(k_stride, (long)Hkv * D, esize) || !stride_ok(v_stride, (long)Hkv * D, esize))
+        return fail(MEDUSA_ERR_INVALID_ARG,
+                    "kv_append_paged: row strides %lld, %lld below Hkv * D = %d or not a multiple of 16 bytes",
+                    (long long)k_stride, (long long)v_stride, Hkv * D);
+    if (!al16(k) || !al16(v) || !al16(k_pages) || !al16(v_pages))
+        return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_paged: tensors must be 16-byte aligned");
+    if ((uintptr_t)slot_map & 7u)
+        return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_paged: slot_map must be 8-byte aligned");
+    KvAppendArgs a;
+    a.k = k;
+    a.v = v;
+    a.k_stride = k_stride * esize;
+    a.v_stride = v_stride * esize;
+    a.slot_map = slot_map;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.N = N;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.esize = esize;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.status = status;
+    cudaError_t e = kv_append_launch(a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_append_paged launch");
+    return ok();
+}
+
+// the sizes that prompt_attention and chunk_attention_paged share
+static bool prompt_sizes_ok(int B, int N, int max_new, int Hq, int Hkv, int D) {
+    return B >= 1 && N >= 0 && max_new >= 0 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 && Hq / Hkv <= 64 &&
+           (D == 64 || D == 128);
+}
+
+extern "C" size_t prompt_attention_workspace_size(int B, int N, int max_len, int Hq, int Hkv, int D,
+                                                  medusa_dtype dt) {
+    if (!prompt_sizes_ok(B, N, max_len, Hq, Hkv, D)) return 0;
+    if (max_len == 0 || max_len > N) max_len = N;
+    return prompt_workspace_size(B, N, max_len, 0, Hq, Hkv, D, 0, dt);
+}
+
+extern "C" size_t chunk_attention_paged_workspace_size(int B, int N, int max_new, int max_prefix, int max_pages,
+                                                       int page_size, int Hq, int Hkv, int D, medusa_dtype dt) {
+    if (!prompt_sizes_ok(B, N, max_new, Hq, Hkv, D) || max_pages < 1 || page_size < 1 ||
+        (long)max_pages * page_size > (1L << 30))
+        return 0;
+    if (max_new == 0 || max_new > N) max_new = N;
+    if (max_prefix <= 0) max_prefix = max_pages * page_size;
+    return prompt_workspace_size(B, N, max_new, max_prefix, Hq, Hkv, D, page_size, dt);
+}
+
+// prompt_attention and chunk_attention_paged (block_table non-NULL)
+static int prompt_common(const char* fn, PromptArgs& a, size_t workspace_bytes, cudaStream_t st) {
+    if (a.dt != MEDUSA_F32 && a.dt != MEDUSA_BF16) return fail(MEDUSA_ERR_UNSUPPORTED, "%s: unknown dtype", fn);
+    if ((a.N != 0 && (!a.q || !a.k || !a.v || !a.out)) || !a.row_start)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: NULL tensor argument", fn);
+    if (a.B < 1 || a.N < 0 || a.max_new < 0 || a.Hq < 1 || a.Hkv < 1 || a.Hq % a.Hkv || a.Hq > 65535 ||
+        (long)a.N * a.Hq > (1L << 31) - 1)
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: bad sizes B=%d N=%d max=%d Hq=%d Hkv=%d", fn, a.B, a.N, a.max_new,
+                    a.Hq, a.Hkv);
+    if (a.D != 64 && a.D != 128) return fail(MEDUSA_ERR_UNSUPPORTED, "%s: head_dim %d (64 or 128)", fn, a.D);
+    if (a.Hq / a.Hkv > 64)
+        return fail(MEDUSA_ERR_UNSUPPORTED, "%s: %d query heads per kv-head (at most 64)", fn, a.Hq / a.Hkv);
+    const int esize = a.dt == MEDUSA_F32 ? 4 : 2;
+    if (!stride_ok(a.q_stride, (long)a.Hq * a.D, esize) ||
+        (!a.block_table && (!stride_ok(a.k_stride, (long)a.Hkv * a.D, esize) ||
+                            !stride_ok(a.v_stride, (long)a.Hkv * a.D, esize))))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: a row stride is below its row or not a multiple of 16 bytes", fn);
+    if (!al16(a.q) || !al16(a.k) || !al16(a.v) || !al16(a.out))
+        return fail(MEDUSA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+    if (a.max_new == 0 || a.max_new > a.N) a.max_new = a.N;
+    const size_t need =
+        prompt_workspace_size(a.B, a.N, a.max_new, a.max_prefix, a.Hq, a.Hkv, a.D, a.page_size, a.dt);
+    if (need && (!a.ws || workspace_bytes < need || !al16(a.ws)))
+        return fail(MEDUSA_ERR_WORKSPACE, "%s: workspace of %zu bytes, need %zu (16-byte aligned)", fn,
+                    workspace_bytes, need);
+    if (!(a.scale > 0.f)) a.scale = a.D == 128 ? 0.08838834764831845f : 0.125f;
+    cudaError_t e = prompt_launch(a, st);
+    if (e != cudaSuccess) return cuda_fail(e, fn);
+    return ok();
+}
+
+extern "C" int prompt_attention(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                                int64_t v_stride, const int32_t* row_start, int B, int N, int max_len, int Hq,
+                                int Hkv, int D, float scale, medusa_dtype dt, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, int32_t* status, medusa_stream_t stream) {
+    PromptArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.row_start = row_start;
+    a.prefix_len = nullptr;
+    a.block_table = nullptr;
+    a.max_pages = a.page_size = a.num_pages = 0;
+    a.B = B;
+    a.N = N;
+    a.max_new = max_len;
+    a.max_prefix = 0;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.scale = scale;
+    a.dt = dt;
+    a.out = out;
+    a.lse = lse;
+    a.ws = workspace;
+    a.status = status;
+    return prompt_common("prompt_attention", a, workspace_bytes, (cudaStream_t)stream);
+}
+
+extern "C" int chunk_attention_paged(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages,
+                                     const int32_t* block_table, int max_pages, int page_size, int num_pages,
+                                     const int32_t* row_start, const int32_t* prefix_len, int B, int N, int max_new,
+                                     int max_prefix, int Hq, int Hkv, int D, float scale, medusa_dtype dt, void* out,
+                                     float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                                     medusa_stream_t stream) {
+    if (!block_table || !prefix_len)
+        return fail(MEDUSA_ERR_INVALID_ARG, "chunk_attention_paged: NULL tensor argument");
+    if (max_pages < 1 || page_size < 1 || num_pages < 1 || (long)max_pages * page_size > (1L << 30))
+        return fail(MEDUSA_ERR_INVALID_ARG, "chunk_attention_paged: bad sizes max_pages=%d page_size=%d num_pages=%d",
+                    max_pages, page_size, num_pages);
+    const int cap = max_pages * page_size;
+    if (max_prefix <= 0) max_prefix = cap;
+    if (max_prefix > cap)
+        return fail(MEDUSA_ERR_INVALID_ARG, "chunk_attention_paged: max_prefix %d > max_pages * page_size = %d",
+                    max_prefix, cap);
+    PromptArgs a;
+    a.q = q;
+    a.k = k_pages;
+    a.v = v_pages;
+    a.q_stride = q_stride;
+    a.k_stride = a.v_stride = 0;
+    a.row_start = row_start;
+    a.prefix_len = prefix_len;
+    a.block_table = block_table;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.B = B;
+    a.N = N;
+    a.max_new = max_new;
+    a.max_prefix = max_prefix;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.scale = scale;
+    a.dt = dt;
+    a.out = out;
+    a.lse = lse;
+    a.ws = workspace;
+    a.status = status;
+    return prompt_common("chunk_attention_paged", a, workspace_bytes, (cudaStream_t)stream);
+}

@@ -145,6 +145,59 @@ struct CompactArgs {
 };
 cudaError_t compact_launch(const CompactArgs& a, cudaStream_t st);
 
+// ------------------------------- pages -------------------------------------
+constexpr int kMaxPlanSeqs = 8192;  // sequences of one page plan (their lengths are scanned in shared memory)
+struct PagePlanArgs {
+    const int32_t* prefix_len;
+    const int32_t* new_len;
+    int32_t* block_table;
+    const int32_t* owned;
+    int32_t* free_list;
+    const int32_t* free_count;
+    int32_t* owned_out;       // may alias owned
+    int32_t* free_count_out;  // may alias free_count
+    int32_t* row_start;       // [B + 1]
+    int64_t* slot_map;        // [max_tokens]
+    int B, room, max_pages, page_size, num_pages, max_tokens;
+    int32_t* status;
+};
+cudaError_t page_plan_launch(const PagePlanArgs& a, cudaStream_t st);
+struct KvAppendArgs {
+    const void* k;
+    const void* v;
+    long k_stride, v_stride;  // bytes between tokens
+    const int64_t* slot_map;
+    void* k_pages;
+    void* v_pages;
+    int N, Hkv, D, esize, page_size, num_pages;
+    int32_t* status;
+};
+cudaError_t kv_append_launch(const KvAppendArgs& a, cudaStream_t st);
+
+// ------------------------ prompt / chunk attention --------------------------
+// causal attention of packed new rows; keys from packed rows (prompts) or
+// from page pools (block_table non-NULL)
+struct PromptArgs {
+    const void* q;
+    const void* k;  // packed rows, or the page pool
+    const void* v;
+    long q_stride, k_stride, v_stride;  // elements between tokens (k, v: packed rows only)
+    const int32_t* row_start;           // [B + 1]
+    const int32_t* prefix_len;          // [B]; NULL: prompts (nothing cached)
+    const int32_t* block_table;
+    int max_pages, page_size, num_pages;
+    int B, N, max_new, max_prefix, Hq, Hkv, D;
+    float scale;  // > 0
+    medusa_dtype dt;
+    void* out;   // [N, Hq, D]
+    float* lse;  // [N, Hq], natural log; nullable
+    void* ws;
+    int32_t* status;
+};
+size_t prompt_workspace_size(int B, int N, int max_new, int max_prefix, int Hq, int Hkv, int D, int page_size,
+                             medusa_dtype dt);
+cudaError_t prompt_launch(const PromptArgs& a, cudaStream_t st);
+
 // limit of the pipeline waits (hand-overs, phases, grid barriers) that the
 // heads and tree attention kernels are given: kWaitLimitNs unless changed by
 // medusa_debug_set_wait_limit; drains of issued copies and MMAs always wait

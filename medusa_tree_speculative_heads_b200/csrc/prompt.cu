@@ -1,0 +1,354 @@
+// Causal attention of packed new rows: whole prompts over their own packed
+// K/V, and chunks of new tokens (one token: plain decoding) over a paged
+// cache that already holds the chunk's K/V.  This file chooses the kernel and
+// holds the CUDA-core one (fp32, and the bf16 shapes the others do not take)
+// and the merge of key splits.
+//
+// For a new token i of sequence b (position p_b + i) and query head h with
+// kv-head g = h / (Hq / Hkv):
+//     O[h] = sum_{j <= p_b + i} softmax_j(scale <q[h], k_j[g]>) v_j[g]
+// by one pass over the keys with a running maximum and sum in fp32.
+#include "prompt_common.cuh"
+
+namespace medusa {
+
+namespace {
+
+constexpr int kSimtThreads = 256;
+constexpr int kSimtKeys = 64;  // keys per chunk
+constexpr int kMaxSplits = 64;
+
+// One CTA takes M = 16 * MI rows (row = token * G + query head of the group)
+// of one (sequence, kv-head) and one split of its key chunks.  A 16 x 16 grid
+// of threads: thread (ty, tx) holds scores of rows ty + 16 i and keys tx + 16
+// j, then output columns 4 tx + 64 c of the same rows, so that a row's maximum
+// and sum stay within half a warp.  Tiles are fp32 in shared memory (rows
+// padded by 4 floats: 16-byte reads of consecutive rows fall on distinct
+// banks); P overlays K.  Bound by the FMA pipe and its shared-memory operands.
+template <typename E, int D, int MI>
+__global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const PromptArgs a, const SplitBuf buf, int T) {
+    constexpr int M = 16 * MI, LD = D + 4, LP = kSimtKeys + 4, V4 = Elt<E>::kVec;
+    extern __shared__ __align__(16) float sm[];
+    float* sQ = sm;
+    float* sK = sQ + M * LD;
+    float* sV = sK + kSimtKeys * LD;
+    float* sP = sK;  // K is read before P is written
+    __shared__ int s_tile[2];
+    __shared__ int s_ok[kSimtKeys];  // the key exists (its page is valid)
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int g = blockIdx.x % a.Hkv, C = gridDim.y, split = blockIdx.y;
+    if (tid < 32) {
+        const PromptTile t = prompt_tile(a, T, blockIdx.x / a.Hkv);
+        if (tid == 0) {
+            s_tile[0] = t.b;
+            s_tile[1] = t.t;
+            if (blockIdx.x == 0 && split == 0)
+                for (int b = 0; b < a.B; ++b)
+                    if (const int bad = prompt_seq(a, b).bad) set_status(a.status, bad);
+        }
+    }
+    __syncthreads();
+    const int b = s_tile[0];
+    if (b < 0) return;
+    const PromptSeq sq = prompt_seq(a, b);
+    const int G = a.Hq / a.Hkv, tok0 = s_tile[1] * T;
+    const int ntok = min(T, sq.n - tok0), rows = ntok * G;
+    const int keys = sq.p + tok0 + ntok;  // the tile's last token sees [0, keys)
+    const int nch = (keys + kSimtKeys - 1) / kSimtKeys;
+    const int c0 = (int)((long)nch * split / C), c1 = (int)((long)nch * (split + 1) / C);
+
+    auto load_row = [&](float* dst, const E* src, int c) {  // 16 bytes of a row, widened
+        float f[V4];
+        Elt<E>::unpack(ld_nc(src + c * V4), f);
+#pragma unroll
+        for (int i = 0; i < V4; i += 4)
+            *reinterpret_cast<float4*>(dst + c * V4 + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    };
+    auto zero_row = [&](float* dst, int c) {
+#pragma unroll
+        for (int i = 0; i < V4; i += 4)
+            *reinterpret_cast<float4*>(dst + c * V4 + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    constexpr int CV = D / V4;  // 16-byte pieces per row
+    for (int e = tid; e < M * CV; e += kSimtThreads) {
+        const int r = e / CV, c = e % CV;
+        if (r < rows)
+            load_row(sQ + r * LD,
+                     (const E*)a.q + (long)(sq.r0 + tok0 + r / G) * a.q_stride + (long)(g * G + r % G) * D, c);
+        else zero_row(sQ + r * LD, c);
+    }
+    int pos[MI];  // the position of each of the thread's rows
+    float m[MI], l[MI], o[MI][D / 16];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        pos[i] = sq.p + tok0 + (ty + 16 * i) / G;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
+    }
+    const float scale2 = a.scale * 1.4426950408889634f;
+    int bad = 0;
+    for (int ch = c0; ch < c1; ++ch) {
+        const int k0 = ch * kSimtKeys;
+        __syncthreads();  // P and V of the previous chunk are read
+        for (int e = tid; e < kSimtKeys * CV; e += kSimtThreads) {
+            const int r = e / CV, c = e % CV, key = k0 + r;
+            const E* ks = nullptr;
+            const E* vs = nullptr;
+            if (key < keys) {
+                if (a.block_table) {
+                    const int page = a.block_table[(long)b * a.max_pages + key / a.page_size];
+                    if (page >= 0 && page < a.num_pages) {
+                        const long at = (((long)page * a.Hkv + g) * a.page_size + key % a.page_size) * D;
+                        ks = (const E*)a.k + at;
+                        vs = (const E*)a.v + at;
+                    } else {
+                        bad = MEDUSA_STATUS_BAD_PAGE;
+                    }
+                } else {
+                    ks = (const E*)a.k + (long)(sq.r0 + key) * a.k_stride + g * D;
+                    vs = (const E*)a.v + (long)(sq.r0 + key) * a.v_stride + g * D;
+                }
+            }
+            if (ks) {
+                load_row(sK + r * LD, ks, c);
+                load_row(sV + r * LD, vs, c);
+            } else {
+                zero_row(sK + r * LD, c);
+                zero_row(sV + r * LD, c);
+            }
+            if (c == 0) s_ok[r] = ks != nullptr;
+        }
+        __syncthreads();
+        float s[MI][4];
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+            float4 qv[MI], kv[4];
+#pragma unroll
+            for (int i = 0; i < MI; ++i) qv[i] = *reinterpret_cast<const float4*>(sQ + (ty + 16 * i) * LD + d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sK + (tx + 16 * j) * LD + d);
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+                    s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
+                    s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+                    s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+                }
+        }
+        __syncthreads();  // K is read: P may overlay it
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = tx + 16 * j;
+                s[i][j] = k0 + r <= pos[i] && s_ok[r] ? s[i][j] * scale2 : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, w));
+            const float mn = fmaxf(m[i], mx);
+            const float mu = mn == -INFINITY ? 0.f : mn;
+            const float al = exp2f(m[i] - mu);
+            float rs = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f(s[i][j] - mu);
+                sP[(ty + 16 * i) * LP + tx + 16 * j] = p;
+                rs += p;
+            }
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) rs += __shfl_xor_sync(kFull, rs, w);
+            l[i] = l[i] * al + rs;
+            m[i] = mn;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) o[i][c] *= al;
+        }
+        __syncthreads();
+        const bool diag = k0 + kSimtKeys > sq.p + tok0 + 1;  // some row does not see some key
+        for (int k = 0; k < kSimtKeys; k += 4) {
+            float4 pv[MI];
+#pragma unroll
+            for (int i = 0; i < MI; ++i) pv[i] = *reinterpret_cast<const float4*>(sP + (ty + 16 * i) * LP + k);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                float4 vv[D / 64];
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    vv[c] = *reinterpret_cast<const float4*>(sV + (k + kk) * LD + 4 * tx + 64 * c);
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    // a later token's V may hold NaN: 0 * NaN must not reach this row
+                    if (diag && k0 + k + kk > pos[i]) continue;
+                    const float p = kk == 0 ? pv[i].x : kk == 1 ? pv[i].y : kk == 2 ? pv[i].z : pv[i].w;
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        o[i][4 * c] = fmaf(p, vv[c].x, o[i][4 * c]);
+                        o[i][4 * c + 1] = fmaf(p, vv[c].y, o[i][4 * c + 1]);
+                        o[i][4 * c + 2] = fmaf(p, vv[c].z, o[i][4 * c + 2]);
+                        o[i][4 * c + 3] = fmaf(p, vv[c].w, o[i][4 * c + 3]);
+                    }
+                }
+            }
+        }
+    }
+    if (bad) set_status(a.status, bad);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int r = ty + 16 * i;
+        if (r >= rows) continue;
+        const long orow = (long)(sq.r0 + tok0 + r / G) * a.Hq + g * G + r % G;
+        const float inv = l[i] > 0.f ? 1.f / l[i] : l[i] == 0.f ? 0.f : l[i];  // a NaN sum stays NaN
+        if (C > 1) {
+            const long prow = (long)split * a.N * a.Hq + orow;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+                *reinterpret_cast<float4*>(buf.o + prow * D + 4 * tx + 64 * c) =
+                    make_float4(o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv, o[i][4 * c + 3] * inv);
+            if (tx == 0) buf.lse2[prow] = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
+            continue;
+        }
+        E* dst = (E*)a.out + orow * D;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) dst[4 * tx + 64 * c + x] = Elt<E>::from_float(o[i][4 * c + x] * inv);
+        if (a.lse && tx == 0)
+            a.lse[orow] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
+    }
+}
+
+// Merge of the splits of each row, in split order; a warp per row.  A split
+// with no visible key has the log2-sum-exp -inf and no weight.
+template <typename E, int D>
+__global__ void __launch_bounds__(256) prompt_combine_kernel(const PromptArgs a, const SplitBuf buf, int C) {
+    const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5), rows = (long)a.N * a.Hq;
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    const int t = (int)(row / a.Hq);
+    // rows of no sequence (behind the last one, past max_new) are left alone
+    if (t < a.row_start[0] || t >= a.row_start[a.B]) return;
+    int lo = 0, hi = a.B - 1;  // the last sequence that starts at or before t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.row_start[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    const PromptSeq sq = prompt_seq(a, lo);
+    if (t < sq.r0 || t >= sq.r0 + sq.n) return;
+    float M = -INFINITY;
+    bool nan = false;
+    for (int s = 0; s < C; ++s) {
+        const float x = buf.lse2[(long)s * rows + row];
+        M = fmaxf(M, x);
+        nan |= x != x;
+    }
+    constexpr int PL = D / 32;
+    float acc[PL], wsum = 0.f;
+#pragma unroll
+    for (int e = 0; e < PL; ++e) acc[e] = 0.f;
+    const float mu = M == -INFINITY ? 0.f : M;
+    for (int s = 0; s < C; ++s) {
+        const float w = exp2f(buf.lse2[(long)s * rows + row] - mu);
+        if (w == 0.f) continue;  // (a NaN weight is not skipped)
+        const float* src = buf.o + ((long)s * rows + row) * D + lane * PL;
+        wsum += w;
+#pragma unroll
+        for (int e = 0; e < PL; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+    }
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+    E* dst = (E*)a.out + row * D + lane * PL;
+#pragma unroll
+    for (int e = 0; e < PL; ++e) dst[e] = Elt<E>::from_float(acc[e] * inv);
+    if (a.lse && lane == 0)
+        a.lse[row] = nan ? NAN : wsum == 0.f ? -INFINITY : (M + log2f(wsum)) * 0.69314718055994531f;
+}
+
+template <typename E, int D, int MI>
+cudaError_t simt_launch(const PromptArgs& a, long tiles, int T, int splits, const SplitBuf& buf, cudaStream_t st) {
+    constexpr int M = 16 * MI;
+    const size_t smem = (size_t)(M + 2 * kSimtKeys) * (D + 4) * 4;
+    static_assert(M * (kSimtKeys + 4) <= kSimtKeys * (D + 4), "P overlays K");
+    auto kern = prompt_simt_kernel<E, D, MI>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    prefer_max_smem(kern);
+    kern<<<dim3((unsigned)(tiles * a.Hkv), splits), kSimtThreads, smem, st>>>(a, buf, T);
+    return cudaGetLastError();
+}
+
+// The plan of a call: rows per tile, tokens per tile, key splits.
+struct PromptPlan {
+    int M, T, splits;
+    long tiles;
+};
+
+PromptPlan simt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hkv) {
+    PromptPlan p;
+    const int G = Hq / Hkv;
+    // up to 16 rows per (sequence, kv-head), decoding, the small tile
+    p.M = (long)max_new * G <= 16 ? 16 : 64;
+    p.T = p.M / G;
+    p.tiles = prompt_tiles(B, N, max_new, p.T);
+    // (not fewer than the packed rows fill: the workspace bound counts on it)
+    const long items = (p.tiles > N / p.T ? p.tiles : N / p.T) * Hkv;
+    const long chunks = ((long)max_prefix + max_new + kSimtKeys - 1) / kSimtKeys;
+    // two CTAs per SM; a split keeps at least two chunks
+    long s = items > 0 ? 2L * num_sms() / items : 1;
+    if (s > chunks / 2) s = chunks / 2;
+    if (s > kMaxSplits) s = kMaxSplits;
+    p.splits = s < 1 ? 1 : (int)s;
+    return p;
+}
+
+template <typename E, int D>
+cudaError_t simt_dispatch(const PromptArgs& a, cudaStream_t st) {
+    const PromptPlan p = simt_plan(a.B, a.N, a.max_new, a.max_prefix, a.Hq, a.Hkv);
+    const SplitBuf buf = split_buf(a.ws, (long)a.N * a.Hq, D, p.splits);
+    cudaError_t e = p.M == 16 ? simt_launch<E, D, 1>(a, p.tiles, p.T, p.splits, buf, st)
+                              : simt_launch<E, D, 4>(a, p.tiles, p.T, p.splits, buf, st);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    return prompt_combine_launch(a, buf, p.splits, st);
+}
+
+}  // namespace
+
+cudaError_t prompt_combine_launch(const PromptArgs& a, const SplitBuf& buf, int splits, cudaStream_t st) {
+    const long rows = (long)a.N * a.Hq;
+    const unsigned blocks = (unsigned)((rows + 7) / 8);
+    if (a.dt == MEDUSA_F32) {
+        if (a.D == 128) prompt_combine_kernel<float, 128><<<blocks, 256, 0, st>>>(a, buf, splits);
+        else prompt_combine_kernel<float, 64><<<blocks, 256, 0, st>>>(a, buf, splits);
+    } else {
+        if (a.D == 128) prompt_combine_kernel<__nv_bfloat16, 128><<<blocks, 256, 0, st>>>(a, buf, splits);
+        else prompt_combine_kernel<__nv_bfloat16, 64><<<blocks, 256, 0, st>>>(a, buf, splits);
+    }
+    return cudaGetLastError();
+}
+
+size_t prompt_workspace_size(int B, int N, int max_new, int max_prefix, int Hq, int Hkv, int D, int page_size,
+                             medusa_dtype dt) {
+    // An upper bound that grows with N (a call with fewer rows may split its
+    // keys more): splits * tiles * Hkv <= 2 CTAs per SM, so the partial rows
+    // are at most the rows of that many tiles, and at most kMaxSplits per row.
+    (void)B, (void)max_new, (void)max_prefix, (void)Hkv, (void)page_size, (void)dt;
+    const long most = 2L * num_sms() * 64, rows = (long)N * Hq * kMaxSplits;
+    const long part = rows < most ? rows : most;
+    return align256((size_t)part * D * 4) + align256((size_t)part * 4);
+}
+
+cudaError_t prompt_launch(const PromptArgs& a, cudaStream_t st) {
+    if (a.N == 0 || a.B == 0) return cudaSuccess;
+    if (a.dt == MEDUSA_F32) return a.D == 128 ? simt_dispatch<float, 128>(a, st) : simt_dispatch<float, 64>(a, st);
+    return a.D == 128 ? simt_dispatch<__nv_bfloat16, 128>(a, st) : simt_dispatch<__nv_bfloat16, 64>(a, st);
+}
+
+}  // namespace medusa

@@ -1,0 +1,143 @@
+// What the prompt and chunk attention kernels share: the packed batch's
+// sequences, the order in which a grid takes its query tiles, and the merge
+// of key splits.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace medusa {
+
+// Sequence b of a packed batch: n new rows from packed row r0 on, at
+// positions p .. p + n - 1.
+struct PromptSeq {
+    int r0, n, p;
+    int bad;  // status bits of lengths outside their ranges (clamped here)
+};
+
+__device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs& a, int b) {
+    PromptSeq s;
+    s.r0 = a.row_start[b];
+    const int r1 = a.row_start[b + 1];
+    s.bad = 0;
+    s.n = r1 - s.r0;
+    if (s.r0 < 0 || r1 < s.r0 || r1 > a.N) {
+        s.bad = MEDUSA_STATUS_BAD_LENGTH;
+        s.n = 0;
+    } else if (s.n > a.max_new) {
+        s.bad = MEDUSA_STATUS_BAD_LENGTH;
+        s.n = a.max_new;
+    }
+    s.p = a.prefix_len ? a.prefix_len[b] : 0;
+    if (s.p < 0 || s.p > a.max_prefix) {
+        s.bad |= MEDUSA_STATUS_BAD_PREFIX;
+        s.p = s.p < 0 ? 0 : a.max_prefix;
+    }
+    if (a.block_table) {  // new rows past the table's last page
+        const long room = (long)a.max_pages * a.page_size - s.p;
+        if (s.n > room) {
+            s.bad |= MEDUSA_STATUS_BAD_LENGTH;
+            s.n = room < 0 ? 0 : (int)room;
+        }
+    }
+    return s;
+}
+
+// Key chunks (of kChunk keys) that tile t (tokens [t * T, (t + 1) * T) of the
+// sequence) attends to.
+constexpr int kWeightKeys = 128;
+
+// Tiles of a sequence with at most w chunks of kWeightKeys keys.
+__device__ __forceinline__ int tiles_upto(int n, int p, int T, int w) {
+    const long room = (long)w * kWeightKeys - p;
+    if (n == 0 || room <= 0) return 0;
+    return room >= n ? (n + T - 1) / T : (int)(room / T);
+}
+
+// The tile that comes idx-th when the tiles of all sequences are ordered by
+// their number of key chunks, the longest first (so that a grid's last CTAs
+// are its shortest), then by sequence.  One warp; every lane returns the
+// result; b < 0: fewer tiles than idx + 1.  The number of chunks is found by
+// bisection on the count of longer tiles, so nothing is stored.
+struct PromptTile {
+    int b, t;
+};
+__device__ inline PromptTile prompt_tile(const PromptArgs& a, int T, int idx) {
+    const int lane = threadIdx.x & 31;
+    int total = 0, lo = 0;
+    int hi = (a.max_prefix + a.max_new + kWeightKeys - 1) / kWeightKeys;
+    PromptSeq mine;  // the lane's sequence when the batch fits a warp
+    mine.r0 = mine.n = mine.p = 0;
+    const bool one = a.B <= 32;
+    if (one && lane < a.B) mine = prompt_seq(a, lane);
+    auto seq = [&](int b) { return one ? mine : prompt_seq(a, b); };
+    auto upto = [&](int w) {  // tiles with at most w chunks
+        int c = 0;
+        for (int b = lane; b < a.B; b += 32) {
+            const PromptSeq s = seq(b);
+            c += tiles_upto(s.n, s.p, T, w);
+        }
+        return __reduce_add_sync(kFull, c);
+    };
+    total = upto(hi);
+    PromptTile r{-1, 0};
+    if (idx >= total) return r;
+    while (lo < hi) {  // the smallest w with at most idx tiles longer than w
+        const int mid = (lo + hi) >> 1;
+        if (total - upto(mid) <= idx) hi = mid;
+        else lo = mid + 1;
+    }
+    int rank = idx - (total - upto(lo));  // among the tiles of lo chunks
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int b = b0 + lane;
+        int first = 0, cnt = 0;
+        if (b < a.B) {
+            const PromptSeq s = seq(b);
+            first = tiles_upto(s.n, s.p, T, lo - 1);
+            cnt = tiles_upto(s.n, s.p, T, lo) - first;
+        }
+        int inc = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const unsigned hit = __ballot_sync(kFull, inc > rank);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            r.b = b0 + src;
+            r.t = __shfl_sync(kFull, first + rank - (inc - cnt), src);
+            return r;
+        }
+        rank -= __shfl_sync(kFull, inc, 31);
+    }
+    return r;
+}
+
+// upper bound of the tiles of T tokens in a batch of at most N rows
+inline long prompt_tiles(int B, int N, int max_new, int T) {
+    const long per = (max_new + T - 1) / T;
+    const long packed = (long)N / T + (B < N ? B : N);
+    return per * B < packed ? per * B : packed;
+}
+
+// Partial results of key splits in the workspace: normalised fp32 rows
+// [splits][N * Hq][D] and their log2-sum-exps [splits][N * Hq].
+struct SplitBuf {
+    float* o;
+    float* lse2;
+};
+inline size_t split_bytes(long rows, int D, int splits) {
+    return splits > 1 ? align256((size_t)splits * rows * D * 4) + align256((size_t)splits * rows * 4) : 0;
+}
+inline SplitBuf split_buf(void* ws, long rows, int D, int splits) {
+    SplitBuf s{nullptr, nullptr};
+    if (splits > 1) {
+        s.o = (float*)ws;
+        s.lse2 = (float*)((char*)ws + align256((size_t)splits * rows * D * 4));
+    }
+    return s;
+}
+cudaError_t prompt_combine_launch(const PromptArgs& a, const SplitBuf& buf, int splits, cudaStream_t st);
+
+}  // namespace medusa
