@@ -17,6 +17,7 @@ namespace {
 constexpr int kSimtThreads = 256;
 constexpr int kSimtKeys = 64;  // keys per chunk
 constexpr int kMaxSplits = 64;
+constexpr int kMaxTileRows = 256;  // rows per CTA of the tensor-core kernel
 
 // One CTA takes M = 16 * MI rows (row = token * G + query head of the group)
 // of one (sequence, kv-head) and one split of its key chunks.  A 16 x 16 grid
@@ -287,22 +288,25 @@ cudaError_t simt_launch(const PromptArgs& a, long tiles, int T, int splits, cons
 
 // The plan of a call: rows per tile, tokens per tile, key splits.
 struct PromptPlan {
+    bool tc;
     int M, T, splits;
     long tiles;
 };
 
-PromptPlan simt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hkv) {
+PromptPlan prompt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hkv, int page_size, medusa_dtype dt) {
     PromptPlan p;
     const int G = Hq / Hkv;
-    // up to 16 rows per (sequence, kv-head), decoding, the small tile
-    p.M = (long)max_new * G <= 16 ? 16 : 64;
-    p.T = p.M / G;
+    p.tc = prompt_tc_supported(page_size, dt);
+    // CUDA cores: up to 16 rows per (sequence, kv-head), decoding, the small tile
+    p.M = p.tc ? kMaxTileRows : (long)max_new * G <= 16 ? 16 : 64;
+    p.T = p.tc ? prompt_tc_tokens(G) : p.M / G;
     p.tiles = prompt_tiles(B, N, max_new, p.T);
     // (not fewer than the packed rows fill: the workspace bound counts on it)
     const long items = (p.tiles > N / p.T ? p.tiles : N / p.T) * Hkv;
-    const long chunks = ((long)max_prefix + max_new + kSimtKeys - 1) / kSimtKeys;
-    // two CTAs per SM; a split keeps at least two chunks
-    long s = items > 0 ? 2L * num_sms() / items : 1;
+    const int keys = p.tc ? prompt_tc_chunk() : kSimtKeys;
+    const long chunks = ((long)max_prefix + max_new + keys - 1) / keys;
+    // one CTA per SM (CUDA cores: two); a split keeps at least two chunks
+    long s = items > 0 ? (p.tc ? 1L : 2L) * num_sms() / items : 1;
     if (s > chunks / 2) s = chunks / 2;
     if (s > kMaxSplits) s = kMaxSplits;
     p.splits = s < 1 ? 1 : (int)s;
@@ -310,10 +314,11 @@ PromptPlan simt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hkv)
 }
 
 template <typename E, int D>
-cudaError_t simt_dispatch(const PromptArgs& a, cudaStream_t st) {
-    const PromptPlan p = simt_plan(a.B, a.N, a.max_new, a.max_prefix, a.Hq, a.Hkv);
+cudaError_t prompt_dispatch(const PromptArgs& a, cudaStream_t st) {
+    const PromptPlan p = prompt_plan(a.B, a.N, a.max_new, a.max_prefix, a.Hq, a.Hkv, a.page_size, a.dt);
     const SplitBuf buf = split_buf(a.ws, (long)a.N * a.Hq, D, p.splits);
-    cudaError_t e = p.M == 16 ? simt_launch<E, D, 1>(a, p.tiles, p.T, p.splits, buf, st)
+    cudaError_t e = p.tc ? prompt_tc_launch(a, p.tiles, p.splits, buf, st)
+                  : p.M == 16 ? simt_launch<E, D, 1>(a, p.tiles, p.T, p.splits, buf, st)
                               : simt_launch<E, D, 4>(a, p.tiles, p.T, p.splits, buf, st);
     if (e != cudaSuccess || p.splits == 1) return e;
     return prompt_combine_launch(a, buf, p.splits, st);
@@ -337,18 +342,19 @@ cudaError_t prompt_combine_launch(const PromptArgs& a, const SplitBuf& buf, int 
 size_t prompt_workspace_size(int B, int N, int max_new, int max_prefix, int Hq, int Hkv, int D, int page_size,
                              medusa_dtype dt) {
     // An upper bound that grows with N (a call with fewer rows may split its
-    // keys more): splits * tiles * Hkv <= 2 CTAs per SM, so the partial rows
-    // are at most the rows of that many tiles, and at most kMaxSplits per row.
+    // keys more): splits * tiles * Hkv is at most one CTA per SM of
+    // kMaxTileRows rows (CUDA cores: two of 64), so the partial rows are at
+    // most the rows of that many tiles, and at most kMaxSplits per row.
     (void)B, (void)max_new, (void)max_prefix, (void)Hkv, (void)page_size, (void)dt;
-    const long most = 2L * num_sms() * 64, rows = (long)N * Hq * kMaxSplits;
+    const long most = (long)num_sms() * kMaxTileRows, rows = (long)N * Hq * kMaxSplits;
     const long part = rows < most ? rows : most;
     return align256((size_t)part * D * 4) + align256((size_t)part * 4);
 }
 
 cudaError_t prompt_launch(const PromptArgs& a, cudaStream_t st) {
     if (a.N == 0 || a.B == 0) return cudaSuccess;
-    if (a.dt == MEDUSA_F32) return a.D == 128 ? simt_dispatch<float, 128>(a, st) : simt_dispatch<float, 64>(a, st);
-    return a.D == 128 ? simt_dispatch<__nv_bfloat16, 128>(a, st) : simt_dispatch<__nv_bfloat16, 64>(a, st);
+    if (a.dt == MEDUSA_F32) return a.D == 128 ? prompt_dispatch<float, 128>(a, st) : prompt_dispatch<float, 64>(a, st);
+    return a.D == 128 ? prompt_dispatch<__nv_bfloat16, 128>(a, st) : prompt_dispatch<__nv_bfloat16, 64>(a, st);
 }
 
 }  // namespace medusa

@@ -138,6 +138,11 @@ inline SplitBuf split_buf(void* ws, long rows, int D, int splits) {
     }
     return s;
 }
+// tensor-core kernel (bf16): tokens per CTA, keys per chunk, launch
+bool prompt_tc_supported(int page_size, medusa_dtype dt);
+int prompt_tc_tokens(int G);
+int prompt_tc_chunk();
+cudaError_t prompt_tc_launch(const PromptArgs& a, long tiles, int splits, const SplitBuf& buf, cudaStream_t st);
 cudaError_t prompt_combine_launch(const PromptArgs& a, const SplitBuf& buf, int splits, cudaStream_t st);
 
 }  // namespace medusa

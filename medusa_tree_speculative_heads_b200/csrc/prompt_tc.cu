@@ -1,0 +1,522 @@
+// Causal attention of packed new rows on the 5th-generation tensor cores
+// (bf16, head_dim 64/128): whole prompts over packed K/V, and chunks of new
+// tokens over a paged cache.
+//
+// One CTA takes two 128-row query tiles of one (sequence, kv-head) -- rows are
+// token-major, row = token * G + (query head of the group), so the G heads of
+// a token share every K/V element; T = 128 / G tokens per tile -- and a run of
+// 128-key chunks.  Per tile and chunk:
+//   S  = Q K^T     tcgen05.mma M=128 N=128 K=D
+//   P  = exp2(S * scale * log2 e - m), masked; bf16, over S's columns in TMEM
+//   O += P V       tcgen05.mma M=128 N=D K=128 (A = P from TMEM, V MN-major)
+// with the running maximum m and sum l of each row in the fp32 registers of
+// its softmax thread.  m is raised only when a chunk exceeds it by more than 8
+// (log2), so P <= 2^8; the thread then rescales its row of O in TMEM.  P is
+// rounded to bf16 (2^-8 relative, as the operands are); l sums it unrounded.
+// Warps: 0 producer (TMA), 1 TMEM allocation and MMA issue, 2-5 softmax of
+// tile 0, 6-9 of tile 1: while one tile's softmax runs, the tensor cores work
+// on the other's PV and next QK.  A chunk costs each tile 2 x 512 tensor
+// cycles (D = 128) and 128 x 128 exponentials, 1024 cycles of the SM's 16 per
+// clock, so the two are balanced and both bound the kernel.
+// The visible keys of a row are 0 .. its position, so only the chunks that
+// reach past the tile's first position need a mask.  In those, V elements
+// that are not finite are cleared in shared memory (0 * NaN must not reach a
+// row that does not see the key) and added back, from global memory, to the
+// rows that do see them.
+// Every pipeline wait is bounded and sets MEDUSA_STATUS_TIMEOUT on expiry.
+#include "prompt_common.cuh"
+#include "tc.cuh"
+#include "tma.h"
+
+namespace medusa {
+
+namespace {
+
+constexpr int kPW = 10;    // 0 producer, 1 MMA, 2-5 and 6-9 softmax
+constexpr int kPM = 128;   // rows of a query tile
+constexpr int kPC = 128;   // keys per chunk
+// K and V chunks share one ring (K0 V0 K1 V1 ...)
+template <int D> constexpr int p_stages() { return D == 128 ? 5 : 8; }
+
+struct PromptTcArgs {
+    CUtensorMap mq;  // q as (D, Hq, N), box (64, G, T)
+    CUtensorMap mk;  // packed: k as (D, Hkv, N), box (64, 1, 128); paged: the pool as
+    CUtensorMap mv;  //   (D, page_size, num_pages * Hkv), box (64, page_rows, 1)
+    PromptArgs p;
+    SplitBuf buf;
+    int G, T, page_rows;
+    float scale_log2;
+    uint64_t wait_ns;
+};
+
+__device__ __forceinline__ float p_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t p_pack(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// MN-major operand as TMA writes a (64 MN x rows K) box with a 128-byte
+// swizzle: 8 K-rows of 128 bytes per 1024-byte group; `lbo`: byte distance to
+// the next 64-element MN block
+__device__ __forceinline__ uint64_t p_mnmajor_desc(uint32_t addr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// sign bits set where a half of w (two bf16) is infinite or NaN
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
+    return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+
+// bf16 pair `w` with its non-finite halves (bits of `bad`) cleared
+__device__ __forceinline__ uint32_t clear2(uint32_t w, uint32_t bad) {
+    return w & ~((bad >> 15) * 0xffffu);
+}
+
+template <int D, bool kTestWaits>
+__global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_constant__ PromptTcArgs a) {
+    const uint64_t wait_ns = kTestWaits ? a.wait_ns : kWaitLimitNs;
+    constexpr int NSUB = D / 64;
+    constexpr int kSub = kPC * 128;            // [128 rows x 64 elements] block
+    constexpr int kTile = NSUB * kSub;         // a Q tile, or a chunk of K or V
+    constexpr int ST = p_stages<D>();
+    constexpr uint32_t kIdescQK = idesc_bf16_f32(kPM, kPC);
+    constexpr uint32_t kIdescPV = idesc_bf16_f32(kPM, D) | (1u << 16);  // B (V) MN-major
+    constexpr uint32_t kTmemCols = 512;        // S: 2 x 128 columns, O: D columns at 256 and 384
+    // 1024-byte aligned when the kernel has no static shared memory (checked)
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* sQ = smem;
+    uint8_t* sKV = sQ + 2 * kTile;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + ST * kTile);
+    uint64_t* q_full = bars;           // [2]
+    uint64_t* kv_full = q_full + 2;    // [ST]
+    uint64_t* kv_empty = kv_full + ST;
+    uint64_t* s_full = kv_empty + ST;  // [2]
+    uint64_t* p_full = s_full + 2;     // [2]
+    uint64_t* o_full = p_full + 2;     // [2] one phase per PV product
+    uint64_t* o_last = o_full + 2;     // [2] a single phase: the tile's last PV
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_last + 2);
+    volatile int* s_tile = reinterpret_cast<volatile int*>(tmem_slot + 1);  // b, t, dirty
+
+    const PromptArgs& p = a.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = blockIdx.x % p.Hkv, C = gridDim.y, split = blockIdx.y;
+    const int T = a.T, G = a.G;
+    if (smem_addr(smem) & 1023u) {  // never expected (uniform over the grid)
+        if (threadIdx.x == 0) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
+        return;
+    }
+    if (warp == 0) {
+        const PromptTile t = prompt_tile(p, 2 * T, blockIdx.x / p.Hkv);
+        if (lane == 0) {
+            s_tile[0] = t.b;
+            s_tile[1] = t.t;
+            s_tile[2] = 0;
+        }
+        if (blockIdx.x == 0 && split == 0)
+            for (int b = lane; b < p.B; b += 32)
+                if (const int bad = prompt_seq(p, b).bad) set_status(p.status, bad);
+    } else if (warp == 1) {
+        tmem_alloc(tmem_slot, kTmemCols);
+    } else if (threadIdx.x == 64) {
+        tma_prefetch_desc(&a.mq);
+        tma_prefetch_desc(&a.mk);
+        tma_prefetch_desc(&a.mv);
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(&kv_full[s], 1);
+            mbar_init(&kv_empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_full[i], 1);
+            mbar_init(&o_last[i], 1);
+        }
+        mbar_fence_init();
+    }
+    tc_fence_before();
+    sync_block();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int b = s_tile[0];
+    const PromptSeq sq = prompt_seq(p, b < 0 ? 0 : b);
+    const int tok0 = s_tile[1] * 2 * T;
+    const int ntok = b < 0 ? 0 : min(2 * T, sq.n - tok0);
+    const int pos0 = sq.p + tok0;                       // the first row's position
+    const int keys = pos0 + ntok;                       // seen by the last row
+    const int nch = b < 0 ? 0 : (keys + kPC - 1) / kPC;  // chunks of the longer tile
+    const int c0 = (int)((long)nch * split / C), c1 = (int)((long)nch * (split + 1) / C);
+    // chunks of each tile within this split
+    auto count = [&](int tile) {
+        const int n = min(T, ntok - tile * T);
+        if (n <= 0) return 0;
+        return max(0, min(c1, (pos0 + tile * T + n + kPC - 1) / kPC) - c0);
+    };
+    const int cnt0 = count(0), cnt1 = count(1), cmax = max(cnt0, cnt1);
+    const bool paged = p.block_table != nullptr;
+
+    if (warp == 0) {
+        // ---------------- producer ----------------
+        if (cmax > 0) {
+            if (lane == 0) {
+#pragma unroll
+                for (int tile = 0; tile < 2; ++tile) {
+                    if ((tile == 0 ? cnt0 : cnt1) == 0) continue;
+                    mbar_arrive_expect_tx(&q_full[tile], (uint32_t)(T * G * 128 * NSUB));
+#pragma unroll
+                    for (int sub = 0; sub < NSUB; ++sub)
+                        tma_load_3d(sQ + tile * kTile + sub * kSub, &a.mq, sub * 64, g * G, sq.r0 + tok0 + tile * T,
+                                    &q_full[tile]);
+                }
+            }
+            // the lane's box of a chunk: 64 elements of page_rows (packed: all 128) keys
+            const int pr = paged ? a.page_rows : kPC, nbox = kPC / pr;
+            const int box = lane / NSUB, sub = lane % NSUB;
+            const bool mine = box < nbox;
+            auto page_of = [&](int j) -> int {  // of the lane's box in chunk j; -1: not loaded
+                const int pos = (c0 + j) * kPC + box * pr;
+                if (!mine || j >= cmax || pos >= keys) return -1;
+                if (!paged) return 0;
+                const int page = p.block_table[(long)b * p.max_pages + pos / p.page_size];
+                if (page >= 0 && page < p.num_pages) return page;
+                set_status(p.status, MEDUSA_STATUS_BAD_PAGE);
+                return -1;
+            };
+            int next = page_of(0), issued = 0;
+            bool ok = true;
+            for (int j = 0; j < cmax && ok; ++j) {
+                const int page = next;
+                next = page_of(j + 1);  // one chunk ahead: in flight during this chunk's waits
+                const unsigned loads = __ballot_sync(kFull, page >= 0);
+                const int pos = (c0 + j) * kPC + box * pr;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int i = 2 * j + kv, s = i % ST;
+                    if (i >= ST && !__all_sync(kFull, mbar_wait(&kv_empty[s], ((i / ST) - 1) & 1, wait_ns))) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[s], (uint32_t)(__popc(loads) * pr * 128));
+                    __syncwarp();
+                    ++issued;
+                    if (page >= 0) {
+                        uint8_t* dst = sKV + s * kTile + sub * kSub + box * pr * 128;
+                        const CUtensorMap* m = kv ? &a.mv : &a.mk;
+                        if (paged) tma_load_3d(dst, m, sub * 64, pos % p.page_size, page * p.Hkv + g, &kv_full[s]);
+                        else tma_load_3d(dst, m, sub * 64, g, sq.r0 + pos, &kv_full[s]);
+                    }
+                }
+            }
+            if (!ok && lane == 0) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
+            // drain: no copy may still be landing when the CTA exits
+            if (cnt0 > 0) mbar_wait(&q_full[0], 0);
+            if (cnt1 > 0) mbar_wait(&q_full[1], 0);
+            for (int i = max(0, issued - ST); i < issued; ++i) mbar_wait(&kv_full[i % ST], (i / ST) & 1);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0 && cmax > 0) {
+            bool ok = true;
+            int done = 0;  // tiles whose last product is issued
+            auto active = [&](int tile, int j) { return j < (tile == 0 ? cnt0 : cnt1); };
+            auto last_tile = [&](int j) { return j < cnt1 ? 1 : 0; };  // the last to use chunk j
+            auto issue_qk = [&](int tile, int j) -> bool {
+                const int i = 2 * j, s = i % ST;
+                if (!mbar_wait(&kv_full[s], (i / ST) & 1, wait_ns)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int sub = 0; sub < NSUB; ++sub) {
+                    const uint64_t ad = sw128_kmajor_desc(smem_addr(sQ + tile * kTile + sub * kSub));
+                    const uint64_t bd = sw128_kmajor_desc(smem_addr(sKV + s * kTile + sub * kSub));
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        tc_mma_bf16(tmem + tile * kPC, ad + 2 * ks, bd + 2 * ks, kIdescQK, (sub | ks) != 0);
+                }
+                tc_commit(&s_full[tile]);
+                if (tile == last_tile(j)) tc_commit(&kv_empty[s]);
+                return true;
+            };
+            for (int tile = 0; tile < 2 && ok; ++tile)
+                if (active(tile, 0)) ok = mbar_wait(&q_full[tile], 0, wait_ns) && issue_qk(tile, 0);
+            for (int j = 0; j < cmax && ok; ++j) {
+                const int i = 2 * j + 1, s = i % ST;
+                for (int tile = 0; tile < 2 && ok; ++tile) {
+                    if (!active(tile, j)) continue;
+                    ok = mbar_wait(&p_full[tile], j & 1, wait_ns) && mbar_wait(&kv_full[s], (i / ST) & 1, wait_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t bd = p_mnmajor_desc(smem_addr(sKV + s * kTile), kSub);
+#pragma unroll
+                    for (int ks = 0; ks < kPC / 16; ++ks)  // 16 keys: 8 columns of P, two 1024-byte groups of V
+                        tc_mma_bf16_ts(tmem + 256 + tile * 128, tmem + tile * kPC + ks * 8,
+                                       bd + (uint64_t)(2048 >> 4) * ks, kIdescPV, (j | ks) != 0);
+                    tc_commit(&o_full[tile]);
+                    if (tile == last_tile(j)) tc_commit(&kv_empty[s]);
+                    if (!active(tile, j + 1)) {
+                        tc_commit(&o_last[tile]);
+                        done |= 1 << tile;
+                    }
+                    // S of the next chunk goes over P: the products run in issue order
+                    else ok = issue_qk(tile, j + 1);
+                }
+            }
+            if (!ok) {
+                // completes once every product issued has finished writing TMEM
+                set_status(p.status, MEDUSA_STATUS_TIMEOUT);
+                for (int tile = 0; tile < 2; ++tile)
+                    if (!(done >> tile & 1)) tc_commit(&o_last[tile]);
+            }
+            if (cnt0 > 0 || !ok) mbar_wait(&o_last[0], 0);
+            if (cnt1 > 0 || !ok) mbar_wait(&o_last[1], 0);
+        }
+    } else {
+        // ---------------- softmax ----------------
+        const int tile = warp >= 6 ? 1 : 0, cnt = tile ? cnt1 : cnt0;
+        const int lr = (warp & 3) * 32 + lane;  // TMEM lane = row of the tile
+        const int tok = tile * T + lr / G;
+        const bool row_ok = lr < T * G && tok < ntok;
+        const int pos = row_ok ? pos0 + tok : -1;  // a row of no token sees no key
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ts = lane_base + tile * kPC, to = lane_base + 256 + tile * 128;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < cnt && ok; ++j) {
+            if (!__all_sync(kFull, mbar_wait(&s_full[tile], j & 1, wait_ns))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const int key0 = (c0 + j) * kPC;
+            uint32_t raw[kPC / 16][16];
+#pragma unroll
+            for (int c = 0; c < kPC / 16; ++c) tmem_ld16_async(ts + c * 16, raw[c]);
+            tmem_wait_ld(raw);
+            const int lim = pos - key0;  // visible: c <= lim
+            if (__any_sync(kFull, lim < kPC - 1)) {
+#pragma unroll
+                for (int c = 0; c < kPC; ++c)
+                    raw[c >> 4][c & 15] = c <= lim ? raw[c >> 4][c & 15] : 0xff800000u;
+            }
+            float m4[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) m4[c] = __uint_as_float(raw[0][c]);
+#pragma unroll
+            for (int c = 4; c < kPC; ++c) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(raw[c >> 4][c & 15]));
+            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+            const bool raise = mx > m + 8.f;
+            const float mn = raise ? mx : m;
+            const float mu = mn == -INFINITY ? 0.f : mn;
+            const float alpha = raise ? p_exp2(m - mu) : 1.f;
+            float r4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < kPC / 32; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int x = c * 32 + 2 * e;
+                    const float p0 = p_exp2(fmaf(__uint_as_float(raw[x >> 4][x & 15]), a.scale_log2, -mu));
+                    const float p1 = p_exp2(fmaf(__uint_as_float(raw[x >> 4][(x & 15) + 1]), a.scale_log2, -mu));
+                    r4[e & 3] += p0 + p1;
+                    pk[e] = p_pack(p0, p1);
+                }
+                tmem_st16(ts + c * 16, pk);
+            }
+            l = l * alpha + ((r4[0] + r4[1]) + (r4[2] + r4[3]));
+            m = mn;
+            if (j >= 1 && __any_sync(kFull, raise)) {  // rescale this warp's rows of O
+                if (!__all_sync(kFull, mbar_wait(&o_full[tile], (j - 1) & 1, wait_ns))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < D / 16; c += 4) {
+                    uint32_t ro[4][16];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) tmem_ld16_async(to + (c + x) * 16, ro[x]);
+                    tmem_wait_ld(ro);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) ro[x][e] = __float_as_uint(__uint_as_float(ro[x][e]) * alpha);
+                        tmem_st16(to + (c + x) * 16, ro[x]);
+                    }
+                }
+            }
+            // the first tile to use a chunk that some row sees only in part clears its V
+            if (key0 + kPC > pos0 + 1 && (tile == 0 || j >= cnt0)) {
+                const int i = 2 * j + 1, s = i % ST;
+                if (!__all_sync(kFull, mbar_wait(&kv_full[s], (i / ST) & 1, wait_ns))) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* row = sKV + s * kTile + lr * 128;
+                if (key0 + lr >= keys) {  // no row sees this key: whatever is there
+#pragma unroll
+                    for (int x = 0; x < NSUB * 8; ++x)
+                        *reinterpret_cast<uint4*>(row + (x >> 3) * kSub + ((x + lr) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+#pragma unroll 4
+                    for (int x = 0; x < NSUB * 8; ++x) {
+                        uint4* at = reinterpret_cast<uint4*>(row + (x >> 3) * kSub + ((x + lr) & 7) * 16);
+                        uint4 w = *at;
+                        const uint32_t b0 = nonfinite2(w.x), b1 = nonfinite2(w.y), b2 = nonfinite2(w.z),
+                                       b3 = nonfinite2(w.w);
+                        if (b0 | b1 | b2 | b3) {
+                            *at = make_uint4(clear2(w.x, b0), clear2(w.y, b1), clear2(w.z, b2), clear2(w.w, b3));
+                            s_tile[2] = 1;
+                        }
+                    }
+                }
+                fence_proxy_async_shared();
+            }
+            tmem_wait_st();  // P (and a rescaled O) in TMEM before the products read it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[tile]);
+        }
+        if (ok && cnt > 0) ok = __all_sync(kFull, mbar_wait(&o_last[tile], 0, wait_ns));
+        if (!ok && lane == 0) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
+        tc_fence_after();
+        if (ok && b >= 0) {
+            float o[D];
+            if (cnt > 0) {
+#pragma unroll
+                for (int c = 0; c < D / 16; c += 4) {
+                    uint32_t ro[4][16];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) tmem_ld16_async(to + (c + x) * 16, ro[x]);
+                    tmem_wait_ld(ro);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[(c + x) * 16 + e] = __uint_as_float(ro[x][e]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < D; ++e) o[e] = 0.f;
+            }
+            // The clearing of a chunk precedes every product on it (of either
+            // tile), so a flag raised for this tile's chunks is visible here.
+            if (s_tile[2] && row_ok) {
+                const int lo = max(c0 * kPC, (pos0 + 1) / kPC * kPC), hi = min(pos + 1, c1 * kPC);
+                for (int key = lo; key < hi; ++key) {
+                    const __nv_bfloat16* vr;
+                    if (paged) {
+                        const int page = p.block_table[(long)b * p.max_pages + key / p.page_size];
+                        if (page < 0 || page >= p.num_pages) continue;
+                        vr = (const __nv_bfloat16*)p.v +
+                             (((long)page * p.Hkv + g) * p.page_size + key % p.page_size) * D;
+                    } else {
+                        vr = (const __nv_bfloat16*)p.v + (long)(sq.r0 + key) * p.v_stride + g * D;
+                    }
+#pragma unroll
+                    for (int e = 0; e < D; e += 8) {
+                        const uint4 w = ld_nc(vr + e);
+                        if (nonfinite2(w.x) | nonfinite2(w.y) | nonfinite2(w.z) | nonfinite2(w.w)) {
+                            float f[8];
+                            Elt<__nv_bfloat16>::unpack(w, f);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                if (!isfinite(f[x])) o[e + x] += f[x];
+                        }
+                    }
+                }
+            }
+            if (row_ok) {
+                const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // a NaN sum stays NaN
+                const long orow = (long)(sq.r0 + tok0 + tok) * p.Hq + g * G + lr % G;
+                if (C > 1) {
+                    const long prow = (long)split * p.N * p.Hq + orow;
+                    float4* dst = reinterpret_cast<float4*>(a.buf.o + prow * D);
+#pragma unroll
+                    for (int e = 0; e < D; e += 4)
+                        dst[e / 4] = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+                    a.buf.lse2[prow] = l == 0.f ? -INFINITY : m + log2f(l);
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)p.out + orow * D);
+#pragma unroll
+                    for (int e = 0; e < D; e += 8)
+                        dst[e / 8] = make_uint4(p_pack(o[e] * inv, o[e + 1] * inv), p_pack(o[e + 2] * inv, o[e + 3] * inv),
+                                                p_pack(o[e + 4] * inv, o[e + 5] * inv),
+                                                p_pack(o[e + 6] * inv, o[e + 7] * inv));
+                    if (p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                }
+            }
+        }
+    }
+    // every role is done: no product in flight, no copy landing
+    tc_fence_before();
+    sync_block();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D>
+constexpr size_t prompt_tc_smem() {
+    return (size_t)(2 + p_stages<D>()) * kPC * D * 2 + (2 + 2 * p_stages<D>() + 8) * 8 + 16;
+}
+static_assert(prompt_tc_smem<128>() <= 232448 && prompt_tc_smem<64>() <= 232448, "shared memory of a CTA");
+
+}  // namespace
+
+bool prompt_tc_supported(int page_size, medusa_dtype dt) {
+    return dt == MEDUSA_BF16 && (page_size == 0 || attn_tc_page_ok(page_size));
+}
+
+int prompt_tc_tokens(int G) { return 2 * (kPM / G); }
+int prompt_tc_chunk() { return kPC; }
+
+cudaError_t prompt_tc_launch(const PromptArgs& x, long tiles, int splits, const SplitBuf& buf, cudaStream_t st) {
+    PromptTcArgs a;
+    const uint64_t D = x.D, Hq = x.Hq, Hkv = x.Hkv, N = x.N;
+    a.G = x.Hq / x.Hkv;
+    a.T = kPM / a.G;
+    {
+        const uint64_t dims[3] = {D, Hq, N}, strides[2] = {D * 2, (uint64_t)x.q_stride * 2};
+        const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.T};
+        if (!make_tmap_bf16(&a.mq, x.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    if (x.block_table) {
+        a.page_rows = x.page_size < 64 ? x.page_size : 64;
+        const uint64_t ps = x.page_size, NP = (uint64_t)x.num_pages * Hkv;
+        const uint64_t dims[3] = {D, ps, NP}, strides[2] = {D * 2, ps * D * 2};
+        const uint32_t box[3] = {64, (uint32_t)a.page_rows, 1};
+        if (!make_tmap_bf16(&a.mk, x.k, 3, dims, strides, box)) return cudaErrorInvalidValue;
+        if (!make_tmap_bf16(&a.mv, x.v, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    } else {
+        a.page_rows = kPC;
+        const uint64_t dims[3] = {D, Hkv, N};
+        const uint64_t ks[2] = {D * 2, (uint64_t)x.k_stride * 2}, vs[2] = {D * 2, (uint64_t)x.v_stride * 2};
+        const uint32_t box[3] = {64, 1, (uint32_t)kPC};
+        if (!make_tmap_bf16(&a.mk, x.k, 3, dims, ks, box)) return cudaErrorInvalidValue;
+        if (!make_tmap_bf16(&a.mv, x.v, 3, dims, vs, box)) return cudaErrorInvalidValue;
+    }
+    a.p = x;
+    a.buf = buf;
+    a.scale_log2 = x.scale * 1.4426950408889634f;
+    a.wait_ns = wait_limit_ns();
+    const bool test = a.wait_ns != kWaitLimitNs;
+    void (*kern)(PromptTcArgs) = x.D == 128 ? (test ? prompt_tc_kernel<128, true> : prompt_tc_kernel<128, false>)
+                                            : (test ? prompt_tc_kernel<64, true> : prompt_tc_kernel<64, false>);
+    const size_t smem = x.D == 128 ? prompt_tc_smem<128>() : prompt_tc_smem<64>();
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3((unsigned)(tiles * x.Hkv), splits), kPW * 32, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace medusa
