@@ -341,18 +341,22 @@ cudaError_t prompt_combine_launch(const PromptArgs& a, const SplitBuf& buf, int 
 
 size_t prompt_workspace_size(int B, int N, int max_new, int max_prefix, int Hq, int Hkv, int D, int page_size,
                              medusa_dtype dt) {
+    (void)max_new;
     // An upper bound that grows with N (a call with fewer rows may split its
     // keys more): splits * tiles * Hkv is at most one CTA per SM of
     // kMaxTileRows rows (CUDA cores: two of 64), so the partial rows are at
     // most the rows of that many tiles, and at most kMaxSplits per row.
-    (void)B, (void)max_new, (void)max_prefix, (void)Hkv, (void)page_size, (void)dt;
+    (void)max_prefix;
     const long most = (long)num_sms() * kMaxTileRows, rows = (long)N * Hq * kMaxSplits;
     const long part = rows < most ? rows : most;
-    return align256((size_t)part * D * 4) + align256((size_t)part * 4);
+    const size_t split = align256((size_t)part * D * 4) + align256((size_t)part * 4);
+    const size_t few = decode_supported(B, 1, Hq, Hkv, page_size, dt) ? decode_workspace_size(D) : 0;
+    return few > split ? few : split;
 }
 
 cudaError_t prompt_launch(const PromptArgs& a, cudaStream_t st) {
     if (a.N == 0 || a.B == 0) return cudaSuccess;
+    if (a.block_table && decode_supported(a.B, a.max_new, a.Hq, a.Hkv, a.page_size, a.dt)) return decode_launch(a, st);
     if (a.dt == MEDUSA_F32) return a.D == 128 ? prompt_dispatch<float, 128>(a, st) : prompt_dispatch<float, 64>(a, st);
     return a.D == 128 ? prompt_dispatch<__nv_bfloat16, 128>(a, st) : prompt_dispatch<__nv_bfloat16, 64>(a, st);
 }

@@ -114,6 +114,16 @@ __device__ inline PromptTile prompt_tile(const PromptArgs& a, int T, int idx) {
     return r;
 }
 
+// sign bits set where a half of w (two bf16) is infinite or NaN
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
+    return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+
+// bf16 pair `w` with its non-finite halves (bits of `bad`) cleared
+__device__ __forceinline__ uint32_t clear2(uint32_t w, uint32_t bad) {
+    return w & ~((bad >> 15) * 0xffffu);
+}
+
 // upper bound of the tiles of T tokens in a batch of at most N rows
 inline long prompt_tiles(int B, int N, int max_new, int T) {
     const long per = (max_new + T - 1) / T;
@@ -143,6 +153,10 @@ bool prompt_tc_supported(int page_size, medusa_dtype dt);
 int prompt_tc_tokens(int G);
 int prompt_tc_chunk();
 cudaError_t prompt_tc_launch(const PromptArgs& a, long tiles, int splits, const SplitBuf& buf, cudaStream_t st);
+// few rows per (sequence, kv-head) over a paged cache (bf16)
+bool decode_supported(int B, int max_new, int Hq, int Hkv, int page_size, medusa_dtype dt);
+size_t decode_workspace_size(int D);
+cudaError_t decode_launch(const PromptArgs& a, cudaStream_t st);
 cudaError_t prompt_combine_launch(const PromptArgs& a, const SplitBuf& buf, int splits, cudaStream_t st);
 
 }  // namespace medusa

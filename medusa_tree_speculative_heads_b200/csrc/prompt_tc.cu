@@ -73,16 +73,6 @@ __device__ __forceinline__ uint64_t p_mnmajor_desc(uint32_t addr, uint32_t lbo) 
     return d;
 }
 
-// sign bits set where a half of w (two bf16) is infinite or NaN
-__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
-    return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-}
-
-// bf16 pair `w` with its non-finite halves (bits of `bad`) cleared
-__device__ __forceinline__ uint32_t clear2(uint32_t w, uint32_t bad) {
-    return w & ~((bad >> 15) * 0xffffu);
-}
-
 template <int D, bool kTestWaits>
 __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_constant__ PromptTcArgs a) {
     const uint64_t wait_ns = kTestWaits ? a.wait_ns : kWaitLimitNs;
