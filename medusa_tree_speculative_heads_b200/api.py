@@ -425,37 +425,57 @@ class MedusaStep:
 # prompts and single tokens over the paged cache
 # ----------------------------------------------------------------------------
 
-def _need(ok: bool, msg: str) -> None:
-    if not ok:
-        raise ValueError(msg)
-
-
 def _ints(name: str, t: torch.Tensor, shape, device, dtype=torch.int32) -> None:
-    """An index array: dtype, device, shape (None: any extent), contiguous."""
-    _need(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
-    _need(t.device == device, f"{name} is on {t.device}, expected {device}")
-    _need(t.dim() == len(shape) and all(w is None or w == n for w, n in zip(shape, t.shape)),
-          f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    _need(t.is_contiguous(), f"{name} must be contiguous")
+    """An index array: dtype, device, shape, contiguous.  (These checks run on
+    every call: nothing is formatted unless one fails.)"""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(name: str, t: torch.Tensor, N, heads: int, D: int, dtype, device) -> int:
+def _extent(name: str, t: torch.Tensor, dim: int) -> int:
+    """The last extent of an index array of ``dim`` dimensions."""
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
+    return t.shape[-1]
+
+
+def _rows(name: str, t: torch.Tensor, N: int, heads: int, D: int, dtype, device) -> int:
     """Packed rows [N, heads, D]: a row's heads contiguous, rows any (16-byte
     multiple) stride apart.  Returns the row stride in elements."""
-    _need(t.dim() == 3 and (N is None or t.shape[0] == N) and t.shape[1] == heads and t.shape[2] == D,
-          f"{name} must have shape {[N, heads, D]}, got {list(t.shape)}")
-    _need(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
-    _need(t.device == device, f"{name} is on {t.device}, expected {device}")
-    s = t.stride()
-    _need(t.numel() == 0 or ((s[2] == 1 or D == 1) and (s[1] == D or heads == 1)),
-          f"{name}: the heads of a row must be contiguous, got strides {s}")
-    return s[0] if t.shape[0] > 1 else heads * D
+    if t.shape != (N, heads, D):
+        raise ValueError(f"{name} must have shape {[N, heads, D]}, got {list(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if N < 2 and t.is_contiguous():
+        return heads * D
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and D != 1) or (s1 != D and heads != 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
+    return s0 if N > 1 else heads * D
 
 
-def _pool(name: str, t: torch.Tensor, dtype, device) -> None:
-    _need(t.dim() == 4 and t.is_contiguous(), f"{name} must be a contiguous [num_pages, Hkv, page_size, D] pool")
-    _need(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
-    _need(t.device == device, f"{name} is on {t.device}, expected {device}")
+def _pool(name: str, t: torch.Tensor, shape, dtype, device) -> None:
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [num_pages, Hkv, page_size, D] pool of {list(shape)}, got "
+                         f"{list(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _pool_shape(k_pages: torch.Tensor):
+    if k_pages.dim() != 4:
+        raise ValueError(f"k_pages must be [num_pages, Hkv, page_size, D], got {list(k_pages.shape)}")
+    return k_pages.shape
 
 
 def kv_page_plan(prefix_len, new_len, block_table, owned, free_list, free_count, page_size: int, max_tokens: int,
@@ -469,9 +489,9 @@ def kv_page_plan(prefix_len, new_len, block_table, owned, free_list, free_count,
     B, dev = prefix_len.shape[0], prefix_len.device
     _ints("prefix_len", prefix_len, (B,), dev)
     _ints("new_len", new_len, (B,), dev)
-    _ints("block_table", block_table, (B, None), dev)
+    _ints("block_table", block_table, (B, _extent("block_table", block_table, 2)), dev)
     _ints("owned", owned, (B,), dev)
-    _ints("free_list", free_list, (None,), dev)
+    _ints("free_list", free_list, (_extent("free_list", free_list, 1),), dev)
     _ints("free_count", free_count, (1,), dev)
     out = {
         "row_start": torch.empty((B + 1,), dtype=torch.int32, device=dev),
@@ -487,20 +507,24 @@ def kv_page_plan(prefix_len, new_len, block_table, owned, free_list, free_count,
     return out
 
 
+def _slots(slot_map: torch.Tensor, N: int, device) -> None:
+    _ints("slot_map", slot_map, (_extent("slot_map", slot_map, 1),), device, torch.int64)
+    if slot_map.shape[0] < N:
+        raise ValueError(f"slot_map has {slot_map.shape[0]} entries for {N} rows")
+
+
 def kv_append_paged(k, v, slot_map, k_pages, v_pages) -> Dict[str, torch.Tensor]:
     """Writes packed K/V rows [N,Hkv,D] (views with any row stride) to their
     slots of the pools [num_pages,Hkv,page_size,D], in place; slot -1 skips a
     row.  ``slot_map`` has at least N entries."""
     dev, dt = k_pages.device, k_pages.dtype
-    _pool("k_pages", k_pages, dt, dev)
-    _pool("v_pages", v_pages, dt, dev)
-    _need(k_pages.shape == v_pages.shape, "k_pages and v_pages must have the same shape")
-    num_pages, Hkv, page_size, D = k_pages.shape
+    num_pages, Hkv, page_size, D = shape = _pool_shape(k_pages)
+    _pool("k_pages", k_pages, shape, dt, dev)
+    _pool("v_pages", v_pages, shape, dt, dev)
     N = k.shape[0]
     ks = _rows("k", k, N, Hkv, D, dt, dev)
     vs = _rows("v", v, N, Hkv, D, dt, dev)
-    _ints("slot_map", slot_map, (None,), dev, torch.int64)
-    _need(slot_map.shape[0] >= N, f"slot_map has {slot_map.shape[0]} entries for {N} rows")
+    _slots(slot_map, N, dev)
     st = _status(dev)
     with torch.cuda.device(dev):
         _b.kv_append_paged(k, v, ks, vs, slot_map, N, k_pages, v_pages, page_size, num_pages, Hkv, D,
@@ -519,8 +543,8 @@ def prompt_attention(q, k, v, row_start, scale: float = 0.0, max_len: int = 0,
     qs = _rows("q", q, N, Hq, D, dt, dev)
     ks = _rows("k", k, N, Hkv, D, dt, dev)
     vs = _rows("v", v, N, Hkv, D, dt, dev)
-    _ints("row_start", row_start, (None,), dev)
-    B = row_start.shape[0] - 1
+    B = _extent("row_start", row_start, 1) - 1
+    _ints("row_start", row_start, (B + 1,), dev)
     out = {"out": torch.zeros((N, Hq, D), dtype=dt, device=dev), "status": _status(dev)}
     if want_lse:
         out["lse"] = torch.zeros((N, Hq), dtype=torch.float32, device=dev)
@@ -542,15 +566,13 @@ def chunk_attention_paged(q, k_pages, v_pages, block_table, row_start, prefix_le
     N, Hq, D = q.shape
     dev, dt = q.device, q.dtype
     qs = _rows("q", q, N, Hq, D, dt, dev)
-    _pool("k_pages", k_pages, dt, dev)
-    _pool("v_pages", v_pages, dt, dev)
-    _need(k_pages.shape == v_pages.shape and k_pages.shape[3] == D, "k_pages and v_pages must be equal pools of D")
-    num_pages, Hkv, page_size, _ = k_pages.shape
-    B = prefix_len.shape[0]
+    num_pages, Hkv, page_size, _ = _pool_shape(k_pages)
+    _pool("k_pages", k_pages, (num_pages, Hkv, page_size, D), dt, dev)
+    _pool("v_pages", v_pages, (num_pages, Hkv, page_size, D), dt, dev)
+    B, mp = _extent("prefix_len", prefix_len, 1), _extent("block_table", block_table, 2)
     _ints("prefix_len", prefix_len, (B,), dev)
     _ints("row_start", row_start, (B + 1,), dev)
-    _ints("block_table", block_table, (B, None), dev)
-    mp = block_table.shape[1]
+    _ints("block_table", block_table, (B, mp), dev)
     out = {"out": torch.zeros((N, Hq, D), dtype=dt, device=dev), "status": _status(dev)}
     if want_lse:
         out["lse"] = torch.zeros((N, Hq), dtype=torch.float32, device=dev)
@@ -605,7 +627,8 @@ class PromptStep:
         self.ws = _ws(n, dev)
 
     def _tokens(self, t: torch.Tensor) -> int:
-        _need(t.shape[0] <= self.max_tokens, f"{t.shape[0]} rows, the step holds {self.max_tokens}")
+        if t.shape[0] > self.max_tokens:
+            raise ValueError(f"{t.shape[0]} rows, the step holds {self.max_tokens}")
         return t.shape[0]
 
     def _starts(self, row_start) -> torch.Tensor:
@@ -616,9 +639,8 @@ class PromptStep:
 
     def _pools(self, k_pages, v_pages) -> None:
         shape = (self.num_pages, self.Hkv, self.page_size, self.D)
-        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-            _pool(name, t, self.dtype, self.device)
-            _need(t.shape == shape, f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+        _pool("k_pages", k_pages, shape, self.dtype, self.device)
+        _pool("v_pages", v_pages, shape, self.dtype, self.device)
 
     def plan(self, prefix_len, new_len, block_table, owned, free_list, free_count, owned_out=None,
              free_count_out=None):
@@ -627,13 +649,16 @@ class PromptStep:
         dev = self.device
         owned_out = owned if owned_out is None else owned_out
         free_count_out = free_count if free_count_out is None else free_count_out
-        for name, t in (("prefix_len", prefix_len), ("new_len", new_len), ("owned", owned), ("owned_out", owned_out)):
-            _ints(name, t, (self.B,), dev)
+        each = (self.B,)
+        _ints("prefix_len", prefix_len, each, dev)
+        _ints("new_len", new_len, each, dev)
+        _ints("owned", owned, each, dev)
+        _ints("owned_out", owned_out, each, dev)
         _ints("block_table", block_table, (self.B, self.max_pages), dev)
         _ints("free_list", free_list, (self.num_pages,), dev)
         _ints("free_count", free_count, (1,), dev)
         _ints("free_count_out", free_count_out, (1,), dev)
-        with torch.cuda.device(dev):
+        with _b.on_device(dev):
             _b.kv_page_plan(prefix_len, new_len, self.B, self.room, block_table, self.max_pages, self.page_size,
                             self.num_pages, owned, owned_out, free_list, free_count, free_count_out, self.row_start,
                             self.slot_map, self.max_tokens, self.status)
@@ -648,9 +673,8 @@ class PromptStep:
         if slot_map is None:
             slot_map = self.slot_map
         else:
-            _ints("slot_map", slot_map, (None,), self.device, torch.int64)
-            _need(slot_map.shape[0] >= N, f"slot_map has {slot_map.shape[0]} entries for {N} rows")
-        with torch.cuda.device(self.device):
+            _slots(slot_map, N, self.device)
+        with _b.on_device(self.device):
             _b.kv_append_paged(k, v, ks, vs, slot_map, N, k_pages, v_pages, self.page_size, self.num_pages, self.Hkv,
                                self.D, self.dt, self.status)
 
@@ -661,7 +685,7 @@ class PromptStep:
         ks = _rows("k", k, N, self.Hkv, self.D, self.dtype, self.device)
         vs = _rows("v", v, N, self.Hkv, self.D, self.dtype, self.device)
         row_start = self._starts(row_start)
-        with torch.cuda.device(self.device):
+        with _b.on_device(self.device):
             _b.prompt_attention(q, k, v, qs, ks, vs, row_start, self.B, N, self.max_new, self.Hq, self.Hkv, self.D,
                                 self.scale, self.dt, self.out, self.lse, self.ws, self.ws_n, self.status)
 
@@ -673,7 +697,7 @@ class PromptStep:
         _ints("block_table", block_table, (self.B, self.max_pages), self.device)
         _ints("prefix_len", prefix_len, (self.B,), self.device)
         row_start = self._starts(row_start)
-        with torch.cuda.device(self.device):
+        with _b.on_device(self.device):
             _b.chunk_attention_paged(q, qs, k_pages, v_pages, block_table, self.max_pages, self.page_size,
                                      self.num_pages, row_start, prefix_len, self.B, N, self.max_new, self.max_prefix,
                                      self.Hq, self.Hkv, self.D, self.scale, self.dt, self.out, self.lse, self.ws,

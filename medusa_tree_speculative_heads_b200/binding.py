@@ -9,6 +9,7 @@ the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -357,18 +358,39 @@ def kv_commit_paged(k_pages, v_pages, k_tree, v_tree, block_table, max_pages, pa
                                  _p(new_prefix_len), B, T, Hkv, D, dt, _p(status), _stream(stream)))
 
 
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def on_device(device: torch.device):
+    """Context in which ``device`` is the current one (nothing to enter when
+    it already is)."""
+    return _NO_SWITCH if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _a(t: Optional[torch.Tensor]):
+    """A tensor's address as ctypes converts it without a wrapper object."""
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    """The stream's handle; None: the current stream of the tensor's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
 def kv_page_plan(prefix_len, new_len, B, room, block_table, max_pages, page_size, num_pages, owned, owned_out,
                  free_list, free_count, free_count_out, row_start, slot_map, max_tokens, status, stream=None):
-    _check(lib().kv_page_plan(_p(prefix_len), _p(new_len), B, room, _p(block_table), max_pages, page_size, num_pages,
-                              _p(owned), _p(owned_out), _p(free_list), _p(free_count), _p(free_count_out),
-                              _p(row_start), _p(slot_map), max_tokens, _p(status), _stream(stream)))
+    _check(lib().kv_page_plan(_a(prefix_len), _a(new_len), B, room, _a(block_table), max_pages, page_size, num_pages,
+                              _a(owned), _a(owned_out), _a(free_list), _a(free_count), _a(free_count_out),
+                              _a(row_start), _a(slot_map), max_tokens, _a(status), _raw_stream(stream, row_start)))
 
 
 def kv_append_paged(k, v, k_stride, v_stride, slot_map, N, k_pages, v_pages, page_size, num_pages, Hkv, D, dt, status,
                     stream=None):
     """Strides in elements between tokens."""
-    _check(lib().kv_append_paged(_p(k), _p(v), k_stride, v_stride, _p(slot_map), N, _p(k_pages), _p(v_pages),
-                                 page_size, num_pages, Hkv, D, dt, _p(status), _stream(stream)))
+    _check(lib().kv_append_paged(_a(k), _a(v), k_stride, v_stride, _a(slot_map), N, _a(k_pages), _a(v_pages),
+                                 page_size, num_pages, Hkv, D, dt, _a(status), _raw_stream(stream, k_pages)))
 
 
 def prompt_attention_workspace_size(B, N, max_len, Hq, Hkv, D, dt) -> int:
@@ -377,9 +399,9 @@ def prompt_attention_workspace_size(B, N, max_len, Hq, Hkv, D, dt) -> int:
 
 def prompt_attention(q, k, v, q_stride, k_stride, v_stride, row_start, B, N, max_len, Hq, Hkv, D, scale, dt, out, lse,
                      workspace, workspace_bytes, status, stream=None):
-    _check(lib().prompt_attention(_p(q), _p(k), _p(v), q_stride, k_stride, v_stride, _p(row_start), B, N, max_len, Hq,
-                                  Hkv, D, float(scale), dt, _p(out), _p(lse), _p(workspace), workspace_bytes,
-                                  _p(status), _stream(stream)))
+    _check(lib().prompt_attention(_a(q), _a(k), _a(v), q_stride, k_stride, v_stride, _a(row_start), B, N, max_len, Hq,
+                                  Hkv, D, scale, dt, _a(out), _a(lse), _a(workspace), workspace_bytes, _a(status),
+                                  _raw_stream(stream, row_start)))
 
 
 def chunk_attention_paged_workspace_size(B, N, max_new, max_prefix, max_pages, page_size, Hq, Hkv, D, dt) -> int:
@@ -389,7 +411,7 @@ def chunk_attention_paged_workspace_size(B, N, max_new, max_prefix, max_pages, p
 def chunk_attention_paged(q, q_stride, k_pages, v_pages, block_table, max_pages, page_size, num_pages, row_start,
                           prefix_len, B, N, max_new, max_prefix, Hq, Hkv, D, scale, dt, out, lse, workspace,
                           workspace_bytes, status, stream=None):
-    _check(lib().chunk_attention_paged(_p(q), q_stride, _p(k_pages), _p(v_pages), _p(block_table), max_pages,
-                                       page_size, num_pages, _p(row_start), _p(prefix_len), B, N, max_new, max_prefix,
-                                       Hq, Hkv, D, float(scale), dt, _p(out), _p(lse), _p(workspace), workspace_bytes,
-                                       _p(status), _stream(stream)))
+    _check(lib().chunk_attention_paged(_a(q), q_stride, _a(k_pages), _a(v_pages), _a(block_table), max_pages,
+                                       page_size, num_pages, _a(row_start), _a(prefix_len), B, N, max_new, max_prefix,
+                                       Hq, Hkv, D, scale, dt, _a(out), _a(lse), _a(workspace), workspace_bytes,
+                                       _a(status), _raw_stream(stream, k_pages)))
