@@ -305,9 +305,11 @@ PromptPlan prompt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hk
     const long items = (p.tiles > N / p.T ? p.tiles : N / p.T) * Hkv;
     const int keys = p.tc ? prompt_tc_chunk() : kSimtKeys;
     const long chunks = ((long)max_prefix + max_new + keys - 1) / keys;
-    // one CTA per SM (CUDA cores: two); a split keeps at least two chunks
+    // one CTA per SM (CUDA cores: two); a split keeps at least 8 of the tensor-core
+    // kernel's chunks (the merge launch costs about as much as 4 of them), or 2
     long s = items > 0 ? (p.tc ? 1L : 2L) * num_sms() / items : 1;
-    if (s > chunks / 2) s = chunks / 2;
+    const long most = chunks / (p.tc ? 8 : 2);
+    if (s > most) s = most;
     if (s > kMaxSplits) s = kMaxSplits;
     p.splits = s < 1 ? 1 : (int)s;
     return p;

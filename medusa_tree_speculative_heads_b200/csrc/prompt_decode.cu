@@ -516,12 +516,16 @@ __global__ void __launch_bounds__(kDThreads, kDCtasPerSm) decode_kernel(const __
     if (!ok && lane == 0) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
 }
 
-// Merge of the pairs that several runs share, in run order: a block per
-// (kv-head, sequence), a warp per row.
+// Merge of the pairs that several runs share: a block per (kv-head, sequence,
+// row).  Warp w takes partials w, w + 4, ... in order, its lanes the columns;
+// the four sums are added in order.
+constexpr int kMergeWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(256) decode_merge_kernel(const __grid_constant__ DecodeArgs a, int grid) {
+__global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __grid_constant__ DecodeArgs a, int grid) {
+    constexpr int PL = D / 32;
+    __shared__ float s_acc[kMergeWarps][D], s_w[kMergeWarps];
     const PromptArgs& p = a.p;
-    const int g = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = blockIdx.x, b = blockIdx.y, r = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const PromptSeq sq = prompt_seq(p, b);
     const int nch = decode_chunks(sq), rows = sq.n * a.G;
     long total;
@@ -531,34 +535,38 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const __grid_constant
     const int first = nch ? run_of(total, u0, n_runs) : 0, last = nch ? run_of(total, u0 + nch - 1, n_runs) : 0;
     // every block waits for the runs, so this launch never ends before them
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (first == last || warp >= rows) return;  // (a pair of one run was written by it)
-    constexpr int PL = D / 32;
-    auto slot = [&](int i) { return 2 * i + (i == first ? 1 : 0); };
-    for (int r = warp; r < rows; r += 8) {
-        float M = -INFINITY;
-        for (int i = first + lane; i <= last; i += 32) M = fmaxf(M, a.part_lse2[slot(i) * kDR + r]);
+    if (first == last || r >= rows) return;  // (a pair of one run was written by it)
+    auto slot = [&](int i) { return (long)(2 * i + (i == first ? 1 : 0)) * kDR + r; };
+    float M = -INFINITY;
+    for (int i = first + lane; i <= last; i += 32) M = fmaxf(M, a.part_lse2[slot(i)]);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-        const float mu = M == -INFINITY ? 0.f : M;
-        float acc[PL], wsum = 0.f;
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    const float mu = M == -INFINITY ? 0.f : M;
+    float acc[PL], wsum = 0.f;
 #pragma unroll
-        for (int e = 0; e < PL; ++e) acc[e] = 0.f;
+    for (int e = 0; e < PL; ++e) acc[e] = 0.f;
 #pragma unroll 4
-        for (int i = first; i <= last; ++i) {
-            const float w = d_exp2(a.part_lse2[slot(i) * kDR + r] - mu);
-            const float* src = a.part_o + ((long)slot(i) * kDR + r) * D + lane * PL;
-            wsum += w;
+    for (int i = first + warp; i <= last; i += kMergeWarps) {
+        const float w = d_exp2(a.part_lse2[slot(i)] - mu);
+        const float* src = a.part_o + slot(i) * D + lane * PL;
+        wsum += w;
 #pragma unroll
-            for (int e = 0; e < PL; ++e) acc[e] = fmaf(w, src[e], acc[e]);
-        }
-        const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-        const long orow = (long)(sq.r0 + r / a.G) * p.Hq + g * a.G + r % a.G;
-        uint32_t* dst = reinterpret_cast<uint32_t*>((__nv_bfloat16*)p.out + orow * D + lane * PL);
-#pragma unroll
-        for (int e = 0; e < PL; e += 2) dst[e / 2] = d_pack(acc[e] * inv, acc[e + 1] * inv);
-        if (p.lse && lane == 0)
-            p.lse[orow] = wsum == 0.f ? -INFINITY : (M + log2f(wsum)) * 0.69314718055994531f;
+        for (int e = 0; e < PL; ++e) acc[e] = fmaf(w, src[e], acc[e]);
     }
+#pragma unroll
+    for (int e = 0; e < PL; ++e) s_acc[warp][lane * PL + e] = acc[e];
+    if (lane == 0) s_w[warp] = wsum;
+    __syncthreads();
+    const float L = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const long orow = (long)(sq.r0 + r / a.G) * p.Hq + g * a.G + r % a.G;
+    const int col = threadIdx.x;
+    if (col < D) {
+        const float x = (s_acc[0][col] + s_acc[1][col]) + (s_acc[2][col] + s_acc[3][col]);
+        ((__nv_bfloat16*)p.out)[orow * D + col] = __float2bfloat16_rn(x * inv);
+    }
+    if (p.lse && threadIdx.x == 0)
+        p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
 template <int D>
@@ -580,8 +588,8 @@ cudaError_t decode_launch_d(const DecodeArgs& a, int runs, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     // the merge may be scheduled while the runs finish; it waits for them itself
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.p.Hkv, a.p.B);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(a.p.Hkv, a.p.B, a.p.max_new * a.G);
+    cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

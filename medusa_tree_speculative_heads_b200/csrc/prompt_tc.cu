@@ -9,15 +9,25 @@
 //   S  = Q K^T     tcgen05.mma M=128 N=128 K=D
 //   P  = exp2(S * scale * log2 e - m), masked; bf16, over S's columns in TMEM
 //   O += P V       tcgen05.mma M=128 N=D K=128 (A = P from TMEM, V MN-major)
-// with the running maximum m and sum l of each row in the fp32 registers of
-// its softmax thread.  m is raised only when a chunk exceeds it by more than 8
-// (log2), so P <= 2^8; the thread then rescales its row of O in TMEM.  P is
-// rounded to bf16 (2^-8 relative, as the operands are); l sums it unrounded.
-// Warps: 0 producer (TMA), 1 TMEM allocation and MMA issue, 2-5 softmax of
-// tile 0, 6-9 of tile 1: while one tile's softmax runs, the tensor cores work
-// on the other's PV and next QK.  A chunk costs each tile 2 x 512 tensor
-// cycles (D = 128) and 128 x 128 exponentials, 1024 cycles of the SM's 16 per
-// clock, so the two are balanced and both bound the kernel.
+// with the reference m and the sum l of each row in the fp32 registers of its
+// softmax thread.  P is rounded to bf16 (2^-8 relative, as the operands are);
+// l sums it unrounded.
+// Any m gives the same result as long as nothing overflows, so no maximum is
+// taken after the first chunk: the sum of a chunk's weights bounds them.  When
+// it exceeds 2^8, m is raised by its logarithm, and O in TMEM rescaled, before
+// the next chunk; when the sum of a part of the chunk exceeds 2^32 (or is not a
+// number) the chunk's maximum is taken after all, m raised at once, and the
+// part's weights are computed again.
+// Warps: 0 producer (TMA), 1 and 2 MMA issue of tiles 0 and 1 (1 also TMEM
+// allocation), 4-7 softmax of tile 0, 8-11 of tile 1.  All 512 TMEM columns
+// are in use (2 x 128 of S, 2 x 128 of O), so a tile alternates between its
+// softmax and its products; tile 1 starts a softmax later, so that one tile's
+// softmax runs beside the other's products.  P is handed over in kPParts parts,
+// so that PV runs while the last exponentials are taken.
+// A chunk costs each tile 2 x 512 tensor cycles (D = 128) and 128 x 128
+// exponentials, 1024 cycles of the SM's 16 per clock; what bounds the kernel
+// is the alternation: a tile's softmax (one warp per scheduler) and then two
+// chains of eight products, with a hand-over of some 200 cycles each way.
 // The visible keys of a row are 0 .. its position, so only the chunks that
 // reach past the tile's first position need a mask.  In those, V elements
 // that are not finite are cleared in shared memory (0 * NaN must not reach a
@@ -32,9 +42,11 @@ namespace medusa {
 
 namespace {
 
-constexpr int kPW = 10;    // 0 producer, 1 MMA, 2-5 and 6-9 softmax
+constexpr int kPW = 12;    // warps: 0 producer, 1 and 2 MMA, 4-11 softmax
 constexpr int kPM = 128;   // rows of a query tile
+constexpr int kParts = 3;  // most chunks that some row of a CTA sees in part: its 256 tokens and a first chunk
 constexpr int kPC = 128;   // keys per chunk
+constexpr int kPParts = 2; // parts of P
 // K and V chunks share one ring (K0 V0 K1 V1 ...)
 template <int D> constexpr int p_stages() { return D == 128 ? 5 : 8; }
 
@@ -55,9 +67,42 @@ __device__ __forceinline__ float p_exp2(float x) {
     return y;
 }
 
+// two fp32 values in one 64-bit register: the FMA pipe takes both at once
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void split2(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t p_pack(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// a condition whose code belongs out of the way of the hot path
+__device__ __forceinline__ bool rare(bool x) { return __builtin_expect(x, 0); }
+
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 // MN-major operand as TMA writes a (64 MN x rows K) box with a 128-byte
@@ -77,25 +122,27 @@ template <int D, bool kTestWaits>
 __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_constant__ PromptTcArgs a) {
     const uint64_t wait_ns = kTestWaits ? a.wait_ns : kWaitLimitNs;
     constexpr int NSUB = D / 64;
-    constexpr int kSub = kPC * 128;            // [128 rows x 64 elements] block
-    constexpr int kTile = NSUB * kSub;         // a Q tile, or a chunk of K or V
+    constexpr int kQSub = kPM * 128, kQTile = NSUB * kQSub;  // [128 rows x 64 elements] block, a Q tile
+    constexpr int kSub = kPC * 128, kTile = NSUB * kSub;     // [128 keys x 64 elements] block, a chunk of K or V
     constexpr int ST = p_stages<D>();
     constexpr uint32_t kIdescQK = idesc_bf16_f32(kPM, kPC);
     constexpr uint32_t kIdescPV = idesc_bf16_f32(kPM, D) | (1u << 16);  // B (V) MN-major
-    constexpr uint32_t kTmemCols = 512;        // S: 2 x 128 columns, O: D columns at 256 and 384
+    constexpr uint32_t kTmemCols = 512;        // S: 128 columns per tile, O: D columns at 256 and 384
     // 1024-byte aligned when the kernel has no static shared memory (checked)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* sQ = smem;
-    uint8_t* sKV = sQ + 2 * kTile;
+    uint8_t* sKV = sQ + 2 * kQTile;
     uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + ST * kTile);
     uint64_t* q_full = bars;           // [2]
     uint64_t* kv_full = q_full + 2;    // [ST]
     uint64_t* kv_empty = kv_full + ST;
     uint64_t* s_full = kv_empty + ST;  // [2]
-    uint64_t* p_full = s_full + 2;     // [2]
-    uint64_t* o_full = p_full + 2;     // [2] one phase per PV product
+    uint64_t* p_full = s_full + 2;     // [2][kPParts]
+    uint64_t* o_full = p_full + 2 * kPParts;  // [2] one phase per part of a PV product
     uint64_t* o_last = o_full + 2;     // [2] a single phase: the tile's last PV
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_last + 2);
+    uint64_t* v_clean = o_last + 2;    // [kParts] V of the chunks that some row sees in part is cleared
+    uint64_t* stagger = v_clean + kParts;  // tile 0's first softmax is done
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stagger + 1);
     volatile int* s_tile = reinterpret_cast<volatile int*>(tmem_slot + 1);  // b, t, dirty
 
     const PromptArgs& p = a.p;
@@ -124,15 +171,17 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
         tma_prefetch_desc(&a.mv);
         for (int s = 0; s < ST; ++s) {
             mbar_init(&kv_full[s], 1);
-            mbar_init(&kv_empty[s], 1);
+            mbar_init(&kv_empty[s], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            for (int x = 0; x < kPParts; ++x) mbar_init(&p_full[i * kPParts + x], 4);
             mbar_init(&o_full[i], 1);
             mbar_init(&o_last[i], 1);
         }
+        for (int i = 0; i < kParts; ++i) mbar_init(&v_clean[i], 4);
+        mbar_init(stagger, 4);
         mbar_fence_init();
     }
     tc_fence_before();
@@ -156,6 +205,18 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
     const int cnt0 = count(0), cnt1 = count(1), cmax = max(cnt0, cnt1);
     const bool paged = p.block_table != nullptr;
 
+    // Waits of the MMA and softmax warps: after one has expired the chunks are
+    // passed through without waiting (the results mean nothing), so that every
+    // barrier still meets its threads.  Each lane polls for itself.
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int parity) {
+        if (rare(ok && !mbar_try_wait(bar, parity))) ok = mbar_wait(bar, parity, wait_ns);
+        __syncwarp();
+    };
+    if (warp < 4) {
+    // Registers: 384 threads are launched with 168 each; the softmax warps take
+    // the others' share (88 + 2 * 208 = 3 * 168).
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
         // ---------------- producer ----------------
         if (cmax > 0) {
@@ -166,7 +227,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                     mbar_arrive_expect_tx(&q_full[tile], (uint32_t)(T * G * 128 * NSUB));
 #pragma unroll
                     for (int sub = 0; sub < NSUB; ++sub)
-                        tma_load_3d(sQ + tile * kTile + sub * kSub, &a.mq, sub * 64, g * G, sq.r0 + tok0 + tile * T,
+                        tma_load_3d(sQ + tile * kQTile + sub * kQSub, &a.mq, sub * 64, g * G, sq.r0 + tok0 + tile * T,
                                     &q_full[tile]);
                 }
             }
@@ -184,7 +245,6 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                 return -1;
             };
             int next = page_of(0), issued = 0;
-            bool ok = true;
             for (int j = 0; j < cmax && ok; ++j) {
                 const int page = next;
                 next = page_of(j + 1);  // one chunk ahead: in flight during this chunk's waits
@@ -214,169 +274,207 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
             if (cnt1 > 0) mbar_wait(&q_full[1], 0);
             for (int i = max(0, issued - ST); i < issued; ++i) mbar_wait(&kv_full[i % ST], (i / ST) & 1);
         }
-    } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
-        if (lane == 0 && cmax > 0) {
-            bool ok = true;
-            int done = 0;  // tiles whose last product is issued
-            auto active = [&](int tile, int j) { return j < (tile == 0 ? cnt0 : cnt1); };
-            auto last_tile = [&](int j) { return j < cnt1 ? 1 : 0; };  // the last to use chunk j
-            auto issue_qk = [&](int tile, int j) -> bool {
-                const int i = 2 * j, s = i % ST;
-                if (!mbar_wait(&kv_full[s], (i / ST) & 1, wait_ns)) return false;
-                tc_fence_after();
-#pragma unroll
-                for (int sub = 0; sub < NSUB; ++sub) {
-                    const uint64_t ad = sw128_kmajor_desc(smem_addr(sQ + tile * kTile + sub * kSub));
-                    const uint64_t bd = sw128_kmajor_desc(smem_addr(sKV + s * kTile + sub * kSub));
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        tc_mma_bf16(tmem + tile * kPC, ad + 2 * ks, bd + 2 * ks, kIdescQK, (sub | ks) != 0);
-                }
-                tc_commit(&s_full[tile]);
-                if (tile == last_tile(j)) tc_commit(&kv_empty[s]);
-                return true;
+    } else if (warp < 3) {
+        // ---------------- MMA issuer of a tile ----------------
+        // A warp per tile, so that the waits of one do not hold up the other's
+        // products.  The whole warp runs the loop, so that descriptors and
+        // addresses stay in uniform registers; one elected lane issues.
+        const int tile = warp - 1;
+        const int n = __shfl_sync(kFull, tile ? cnt1 : cnt0, 0), other = __shfl_sync(kFull, tile ? cnt0 : cnt1, 0);
+        if (n > 0) {
+            const bool lead = elect_one();
+            const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+            // a stage is free after one arrival for each tile (two of the only one that uses it)
+            auto release = [&](int s, int j) {
+                tc_commit(&kv_empty[s]);
+                if (j >= other) tc_commit(&kv_empty[s]);
             };
-            for (int tile = 0; tile < 2 && ok; ++tile)
-                if (active(tile, 0)) ok = mbar_wait(&q_full[tile], 0, wait_ns) && issue_qk(tile, 0);
-            for (int j = 0; j < cmax && ok; ++j) {
-                const int i = 2 * j + 1, s = i % ST;
-                for (int tile = 0; tile < 2 && ok; ++tile) {
-                    if (!active(tile, j)) continue;
-                    ok = mbar_wait(&p_full[tile], j & 1, wait_ns) && mbar_wait(&kv_full[s], (i / ST) & 1, wait_ns);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t bd = p_mnmajor_desc(smem_addr(sKV + s * kTile), kSub);
+            const uint64_t qd = sw128_kmajor_desc(smem_addr(sQ) + tile * kQTile), kd = sw128_kmajor_desc(smem_addr(sKV));
+            const uint64_t vd = p_mnmajor_desc(smem_addr(sKV), kSub);
+            const uint32_t t_s = tm + tile * kPC, t_o = tm + 256 + tile * 128;
+            auto issue_qk = [&](int j) {
+                const int i = 2 * j, s = i % ST;
+                wait(&kv_full[s], (i / ST) & 1);
+                tc_fence_after();
+                if (lead) {
 #pragma unroll
-                    for (int ks = 0; ks < kPC / 16; ++ks)  // 16 keys: 8 columns of P, two 1024-byte groups of V
-                        tc_mma_bf16_ts(tmem + 256 + tile * 128, tmem + tile * kPC + ks * 8,
-                                       bd + (uint64_t)(2048 >> 4) * ks, kIdescPV, (j | ks) != 0);
-                    tc_commit(&o_full[tile]);
-                    if (tile == last_tile(j)) tc_commit(&kv_empty[s]);
-                    if (!active(tile, j + 1)) {
-                        tc_commit(&o_last[tile]);
-                        done |= 1 << tile;
-                    }
-                    // S of the next chunk goes over P: the products run in issue order
-                    else ok = issue_qk(tile, j + 1);
+                    for (int sub = 0; sub < NSUB; ++sub)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc_mma_bf16(t_s, qd + (uint64_t)((sub * kQSub) >> 4) + 2 * ks,
+                                        kd + (uint64_t)((s * kTile + sub * kSub) >> 4) + 2 * ks, kIdescQK, (sub | ks) != 0);
+                    // completes after this tile's products so far: its last PV too
+                    tc_commit(&s_full[tile]);
+                    release(s, j);
                 }
+                __syncwarp();
+            };
+            wait(&q_full[tile], 0);
+            issue_qk(0);
+            for (int j = 0; j < n; ++j) {
+                const int i = 2 * j + 1, s = i % ST;
+                const uint64_t bd = vd + (uint64_t)((s * kTile) >> 4);
+                auto pv = [&](int ks) {  // 16 keys: 8 columns of P, two 1024-byte groups of V
+                    tc_mma_bf16_ts(t_o, t_s + ks * 8, bd + (uint64_t)(2048 >> 4) * ks, kIdescPV, (j | ks) != 0);
+                };
+                wait(&kv_full[s], (i / ST) & 1);
+                const int part = c0 + j - (pos0 + 1) / kPC;
+                if (part >= 0) wait(&v_clean[part], 0);
+#pragma unroll
+                for (int x = 0; x < kPParts; ++x) {
+                    constexpr int kSteps = kPC / 16 / kPParts;
+                    wait(&p_full[tile * kPParts + x], j & 1);
+                    tc_fence_after();
+                    if (lead) {
+#pragma unroll
+                        for (int ks = 0; ks < kSteps; ++ks) pv(x * kSteps + ks);
+                        tc_commit(&o_full[tile]);
+                    }
+                    __syncwarp();
+                }
+                if (lead) {
+                    release(s, j);
+                    if (j + 1 == n) tc_commit(&o_last[tile]);
+                }
+                __syncwarp();
+                if (j + 1 < n) issue_qk(j + 1);  // over P: the products run in issue order
             }
-            if (!ok) {
-                // completes once every product issued has finished writing TMEM
-                set_status(p.status, MEDUSA_STATUS_TIMEOUT);
-                for (int tile = 0; tile < 2; ++tile)
-                    if (!(done >> tile & 1)) tc_commit(&o_last[tile]);
-            }
-            if (cnt0 > 0 || !ok) mbar_wait(&o_last[0], 0);
-            if (cnt1 > 0 || !ok) mbar_wait(&o_last[1], 0);
+            if (!ok) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
+            mbar_wait(&o_last[tile], 0);  // every product issued has finished writing TMEM
         }
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------- softmax ----------------
-        const int tile = warp >= 6 ? 1 : 0, cnt = tile ? cnt1 : cnt0;
+        const int tile = warp >= 8 ? 1 : 0, cnt = tile ? cnt1 : cnt0;
         const int lr = (warp & 3) * 32 + lane;  // TMEM lane = row of the tile
         const int tok = tile * T + lr / G;
         const bool row_ok = lr < T * G && tok < ntok;
         const int pos = row_ok ? pos0 + tok : -1;  // a row of no token sees no key
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = lane_base + tile * kPC, to = lane_base + 256 + tile * 128;
+        const uint64_t sc2 = f2(a.scale_log2, a.scale_log2);
         float m = -INFINITY, l = 0.f;
-        bool ok = true;
-        for (int j = 0; j < cnt && ok; ++j) {
-            if (!__all_sync(kFull, mbar_wait(&s_full[tile], j & 1, wait_ns))) {
-                ok = false;
-                break;
-            }
+        bool pending = false;  // the last weights were large: m is to be raised by `rise`
+        float rise = 0.f;
+        auto raise = [&](int done) {  // after `done` parts of PV products
+            const float alpha = pending ? p_exp2(-rise) : 1.f;
+            if (pending) m += rise;
+            pending = false;
+            l *= alpha;
+            if (done == 0) return;
+            wait(&o_full[tile], (done - 1) & 1);
             tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t ro[1][16];
+                tmem_ld16_async(to + c * 16, ro[0]);
+                tmem_wait_ld(ro);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ro[0][e] = __float_as_uint(__uint_as_float(ro[0][e]) * alpha);
+                tmem_st16(to + c * 16, ro[0]);
+            }
+        };
+        for (int j = 0; j < cnt; ++j) {
             const int key0 = (c0 + j) * kPC;
+            // the first tile to use a chunk that some row sees only in part clears its V
+            if (rare(key0 + kPC > pos0 + 1 && (tile == 0 || j >= cnt0))) {
+                const int i = 2 * j + 1, s = i % ST;
+                wait(&kv_full[s], (i / ST) & 1);
+                uint8_t* row = sKV + s * kTile + lr * 128;  // a thread per key
+#pragma unroll 2
+                for (int x = 0; x < NSUB * 8; ++x) {
+                    uint4* at = reinterpret_cast<uint4*>(row + (x >> 3) * kSub + ((x + lr) & 7) * 16);
+                    if (key0 + lr >= keys) {  // no row sees this key: whatever is there
+                        *at = make_uint4(0u, 0u, 0u, 0u);
+                        continue;
+                    }
+                    const uint4 w = *at;
+                    const uint32_t b0 = nonfinite2(w.x), b1 = nonfinite2(w.y), b2 = nonfinite2(w.z), b3 = nonfinite2(w.w);
+                    if (b0 | b1 | b2 | b3) {
+                        *at = make_uint4(clear2(w.x, b0), clear2(w.y, b1), clear2(w.z, b2), clear2(w.w, b3));
+                        s_tile[2] = 1;
+                    }
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_clean[c0 + j - (pos0 + 1) / kPC]);
+            }
+            if (tile == 1 && j == 0 && cnt0 > 0) wait(stagger, 0);
+            wait(&s_full[tile], j & 1);
+            tc_fence_after();
             uint32_t raw[kPC / 16][16];
 #pragma unroll
             for (int c = 0; c < kPC / 16; ++c) tmem_ld16_async(ts + c * 16, raw[c]);
             tmem_wait_ld(raw);
             const int lim = pos - key0;  // visible: c <= lim
-            if (__any_sync(kFull, lim < kPC - 1)) {
+            if (rare(__any_sync(kFull, lim < kPC - 1))) {
 #pragma unroll
                 for (int c = 0; c < kPC; ++c)
                     raw[c >> 4][c & 15] = c <= lim ? raw[c >> 4][c & 15] : 0xff800000u;
             }
-            float m4[4];
+            auto row_max = [&] {
+                float m4[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) m4[c] = __uint_as_float(raw[0][c]);
+                for (int c = 0; c < 4; ++c) m4[c] = __uint_as_float(raw[0][c]);
 #pragma unroll
-            for (int c = 4; c < kPC; ++c) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(raw[c >> 4][c & 15]));
-            const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
-            const bool raise = mx > m + 8.f;
-            const float mn = raise ? mx : m;
-            const float mu = mn == -INFINITY ? 0.f : mn;
-            const float alpha = raise ? p_exp2(m - mu) : 1.f;
-            float r4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < kPC / 32; ++c) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int x = c * 32 + 2 * e;
-                    const float p0 = p_exp2(fmaf(__uint_as_float(raw[x >> 4][x & 15]), a.scale_log2, -mu));
-                    const float p1 = p_exp2(fmaf(__uint_as_float(raw[x >> 4][(x & 15) + 1]), a.scale_log2, -mu));
-                    r4[e & 3] += p0 + p1;
-                    pk[e] = p_pack(p0, p1);
-                }
-                tmem_st16(ts + c * 16, pk);
+                for (int c = 4; c < kPC; ++c) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(raw[c >> 4][c & 15]));
+                return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+            };
+            // the first chunk with a score above -inf sets the reference (O and l are still 0)
+            if (rare(__any_sync(kFull, m == -INFINITY && lim >= 0))) {
+                const float mx = row_max();
+                if (m == -INFINITY) m = mx;
             }
-            l = l * alpha + ((r4[0] + r4[1]) + (r4[2] + r4[3]));
-            m = mn;
-            if (j >= 1 && __any_sync(kFull, raise)) {  // rescale this warp's rows of O
-                if (!__all_sync(kFull, mbar_wait(&o_full[tile], (j - 1) & 1, wait_ns))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+            if (rare(__any_sync(kFull, pending))) raise(j * kPParts);
+            float sum = 0.f;
 #pragma unroll
-                for (int c = 0; c < D / 16; c += 4) {
-                    uint32_t ro[4][16];
+            for (int x = 0; x < kPParts; ++x) {
+                constexpr int kPairs = kPC / 2 / kPParts;
+                uint32_t pk[kPairs / 16][16];
+                float part;
+                for (int again = 0;; ++again) {
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    const uint64_t mu2 = f2(-mu, -mu);
+                    uint64_t s2[2] = {0ull, 0ull};
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) tmem_ld16_async(to + (c + x) * 16, ro[x]);
-                    tmem_wait_ld(ro);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) ro[x][e] = __float_as_uint(__uint_as_float(ro[x][e]) * alpha);
-                        tmem_st16(to + (c + x) * 16, ro[x]);
+                    for (int e = 0; e < kPairs; ++e) {
+                        const int k = 2 * (x * kPairs + e);
+                        const uint64_t t = fma2(f2(__uint_as_float(raw[k >> 4][k & 15]),
+                                                   __uint_as_float(raw[k >> 4][(k & 15) + 1])), sc2, mu2);
+                        float p0, p1;
+                        split2(t, p0, p1);
+                        p0 = p_exp2(p0);
+                        p1 = p_exp2(p1);
+                        s2[e & 1] = add2(s2[e & 1], f2(p0, p1));
+                        pk[e >> 4][e & 15] = p_pack(p0, p1);
                     }
+                    float s0, s1;
+                    split2(add2(s2[0], s2[1]), s0, s1);
+                    part = s0 + s1;
+                    // far above the reference, or not a number
+                    if (!rare(__any_sync(kFull, !(part <= 4294967296.f))) || again) break;
+                    const float mx = row_max();
+                    pending = mx > m;
+                    rise = mx - m;
+                    if (pending) sum *= p_exp2(-rise);
+                    raise(j * kPParts + x);
                 }
-            }
-            // the first tile to use a chunk that some row sees only in part clears its V
-            if (key0 + kPC > pos0 + 1 && (tile == 0 || j >= cnt0)) {
-                const int i = 2 * j + 1, s = i % ST;
-                if (!__all_sync(kFull, mbar_wait(&kv_full[s], (i / ST) & 1, wait_ns))) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* row = sKV + s * kTile + lr * 128;
-                if (key0 + lr >= keys) {  // no row sees this key: whatever is there
+                l += part;
+                sum += part;
 #pragma unroll
-                    for (int x = 0; x < NSUB * 8; ++x)
-                        *reinterpret_cast<uint4*>(row + (x >> 3) * kSub + ((x + lr) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                } else {
-#pragma unroll 4
-                    for (int x = 0; x < NSUB * 8; ++x) {
-                        uint4* at = reinterpret_cast<uint4*>(row + (x >> 3) * kSub + ((x + lr) & 7) * 16);
-                        uint4 w = *at;
-                        const uint32_t b0 = nonfinite2(w.x), b1 = nonfinite2(w.y), b2 = nonfinite2(w.z),
-                                       b3 = nonfinite2(w.w);
-                        if (b0 | b1 | b2 | b3) {
-                            *at = make_uint4(clear2(w.x, b0), clear2(w.y, b1), clear2(w.z, b2), clear2(w.w, b3));
-                            s_tile[2] = 1;
-                        }
-                    }
-                }
-                fence_proxy_async_shared();
+                for (int c = 0; c < kPairs / 16; ++c) tmem_st16(ts + x * kPairs + c * 16, pk[c]);
+                tmem_wait_st();  // P (and a rescaled O) in TMEM before the products read it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[tile * kPParts + x]);
             }
-            tmem_wait_st();  // P (and a rescaled O) in TMEM before the products read it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[tile]);
+            if (tile == 0 && j == 0 && lane == 0) mbar_arrive(stagger);
+            pending = sum > 256.f;
+            rise = __log2f(sum);
         }
-        if (ok && cnt > 0) ok = __all_sync(kFull, mbar_wait(&o_last[tile], 0, wait_ns));
+        if (cnt > 0) wait(&o_last[tile], 0);
+        ok = __all_sync(kFull, ok);
         if (!ok && lane == 0) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
         tc_fence_after();
         if (ok && b >= 0) {
@@ -398,7 +496,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                 for (int e = 0; e < D; ++e) o[e] = 0.f;
             }
             // The clearing of a chunk precedes every product on it (of either
-            // tile), so a flag raised for this tile's chunks is visible here.
+            // tile: v_clean), so a flag raised for this tile's chunks is visible here.
             if (s_tile[2] && row_ok) {
                 const int lo = max(c0 * kPC, (pos0 + 1) / kPC * kPC), hi = min(pos + 1, c1 * kPC);
                 for (int key = lo; key < hi; ++key) {
@@ -457,7 +555,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
 
 template <int D>
 constexpr size_t prompt_tc_smem() {
-    return (size_t)(2 + p_stages<D>()) * kPC * D * 2 + (2 + 2 * p_stages<D>() + 8) * 8 + 16;
+    return (size_t)(2 * kPM + p_stages<D>() * kPC) * D * 2 + (2 + 2 * p_stages<D>() + 7 + 2 * kPParts + kParts) * 8 + 16;
 }
 static_assert(prompt_tc_smem<128>() <= 232448 && prompt_tc_smem<64>() <= 232448, "shared memory of a CTA");
 
