@@ -27,32 +27,31 @@ constexpr int kMaxTileRows = 256;  // rows per CTA of the tensor-core kernel
 // padded by 4 floats: 16-byte reads of consecutive rows fall on distinct
 // banks); P overlays K.  Bound by the FMA pipe and its shared-memory operands.
 template <typename E, int D, int MI>
-__global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const PromptArgs a, const SplitBuf buf, int T) {
+__global__ void __launch_bounds__(kSimtThreads, 2) prompt_simt_kernel(const PromptArgs a, const SplitBuf buf, int T, FastDiv div_T) {
     constexpr int M = 16 * MI, LD = D + 4, LP = kSimtKeys + 4, V4 = Elt<E>::kVec;
     extern __shared__ __align__(16) float sm[];
     float* sQ = sm;
     float* sK = sQ + M * LD;
     float* sV = sK + kSimtKeys * LD;
     float* sP = sK;  // K is read before P is written
-    __shared__ int s_tile[2];
+    __shared__ PromptTile s_tile;
     __shared__ int s_ok[kSimtKeys];  // the key exists (its page is valid)
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int g = blockIdx.x % a.Hkv, C = gridDim.y, split = blockIdx.y;
     if (tid < 32) {
-        const PromptTile t = prompt_tile(a, T, blockIdx.x / a.Hkv);
+        const PromptTile t = prompt_tile(a, T, div_T, blockIdx.x / a.Hkv);
         if (tid == 0) {
-            s_tile[0] = t.b;
-            s_tile[1] = t.t;
+            s_tile = t;
             if (blockIdx.x == 0 && split == 0)
                 for (int b = 0; b < a.B; ++b)
                     if (const int bad = prompt_seq(a, b).bad) set_status(a.status, bad);
         }
     }
     __syncthreads();
-    const int b = s_tile[0];
+    const int b = s_tile.b;
     if (b < 0) return;
-    const PromptSeq sq = prompt_seq(a, b);
-    const int G = a.Hq / a.Hkv, tok0 = s_tile[1] * T;
+    const PromptSeq sq = s_tile.s;
+    const int G = a.Hq / a.Hkv, tok0 = s_tile.t * T;
     const int ntok = min(T, sq.n - tok0), rows = ntok * G;
     const int keys = sq.p + tok0 + ntok;  // the tile's last token sees [0, keys)
     const int nch = (keys + kSimtKeys - 1) / kSimtKeys;
@@ -282,7 +281,7 @@ cudaError_t simt_launch(const PromptArgs& a, long tiles, int T, int splits, cons
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     prefer_max_smem(kern);
-    kern<<<dim3((unsigned)(tiles * a.Hkv), splits), kSimtThreads, smem, st>>>(a, buf, T);
+    kern<<<dim3((unsigned)(tiles * a.Hkv), splits), kSimtThreads, smem, st>>>(a, buf, T, fast_div(T));
     return cudaGetLastError();
 }
 
@@ -297,8 +296,13 @@ PromptPlan prompt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hk
     PromptPlan p;
     const int G = Hq / Hkv;
     p.tc = prompt_tc_supported(page_size, dt);
-    // CUDA cores: up to 16 rows per (sequence, kv-head), decoding, the small tile
-    p.M = p.tc ? kMaxTileRows : (long)max_new * G <= 16 ? 16 : 64;
+    // CUDA cores: the small tile for up to 16 rows per (sequence, kv-head),
+    // decoding, and where the large one leaves SMs idle (24 CTAs of 64 rows, three
+    // sequences of up to 149 tokens at 4 heads: 23 us against 13)
+    p.M = p.tc ? kMaxTileRows : 64;
+    if (!p.tc && G <= 16 &&
+        ((long)max_new * G <= 16 || prompt_tiles(B, N, max_new, 64 / G) * Hkv < num_sms()))
+        p.M = 16;
     p.T = p.tc ? prompt_tc_tokens(G) : p.M / G;
     p.tiles = prompt_tiles(B, N, max_new, p.T);
     // (not fewer than the packed rows fill: the workspace bound counts on it)

@@ -3,6 +3,8 @@
 // of key splits.
 #pragma once
 
+#include <limits.h>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -43,58 +45,89 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs& a, int b) {
     return s;
 }
 
-// Key chunks (of kChunk keys) that tile t (tokens [t * T, (t + 1) * T) of the
-// sequence) attends to.
+// Weight of a tile (tokens [t * T, (t + 1) * T) of its sequence): the number
+// of runs of kWeightKeys keys that its last token sees.
 constexpr int kWeightKeys = 128;
 
-// Tiles of a sequence with at most w chunks of kWeightKeys keys.
-__device__ __forceinline__ int tiles_upto(int n, int p, int T, int w) {
-    const long room = (long)w * kWeightKeys - p;
+// exact x / T for 0 <= x < 2^31, 1 <= T <= 256: m = ceil(2^40 / T), whose excess
+// over 2^40 / T (below 1) moves x * m / 2^40 by less than 2^-9 < 1 / T
+struct FastDiv {
+    uint64_t m;
+};
+inline FastDiv fast_div(int T) { return FastDiv{((1ull << 40) + T - 1) / T}; }
+__device__ __forceinline__ int div_by(int x, FastDiv d) { return (int)(((uint64_t)(uint32_t)x * d.m) >> 40); }
+
+// Tiles of a sequence with at most w runs of kWeightKeys.
+__device__ __forceinline__ int tiles_upto(int n, int p, int T, FastDiv d, int w) {
+    const int room = w * kWeightKeys - p;  // (keys stay below 2^30 + 2^30)
     if (n == 0 || room <= 0) return 0;
-    return room >= n ? (n + T - 1) / T : (int)(room / T);
+    return room >= n ? div_by(n - 1, d) + 1 : div_by(room, d);
 }
 
 // The tile that comes idx-th when the tiles of all sequences are ordered by
 // their number of key chunks, the longest first (so that a grid's last CTAs
 // are its shortest), then by sequence.  One warp; every lane returns the
-// result; b < 0: fewer tiles than idx + 1.  The number of chunks is found by
-// bisection on the count of longer tiles, so nothing is stored.
+// result; b < 0: fewer tiles than idx + 1.  The weight is found by bisection
+// on the count of heavier tiles, so nothing is stored.
 struct PromptTile {
     int b, t;
+    PromptSeq s;
 };
-__device__ inline PromptTile prompt_tile(const PromptArgs& a, int T, int idx) {
+__device__ inline PromptTile prompt_tile(const PromptArgs& a, int T, FastDiv d, int idx) {
     const int lane = threadIdx.x & 31;
-    int total = 0, lo = 0;
-    int hi = (a.max_prefix + a.max_new + kWeightKeys - 1) / kWeightKeys;
+    PromptTile r;
+    r.b = -1;
+    r.t = 0;
     PromptSeq mine;  // the lane's sequence when the batch fits a warp
     mine.r0 = mine.n = mine.p = 0;
     const bool one = a.B <= 32;
     if (one && lane < a.B) mine = prompt_seq(a, lane);
+    auto from_lane = [&](const PromptSeq& s, int src) {
+        r.s.r0 = __shfl_sync(kFull, s.r0, src);
+        r.s.n = __shfl_sync(kFull, s.n, src);
+        r.s.p = __shfl_sync(kFull, s.p, src);
+    };
+    if (a.B == 1) {  // its tiles from the last one back
+        from_lane(mine, 0);
+        const int nt = r.s.n > 0 ? div_by(r.s.n - 1, d) + 1 : 0;
+        if (idx < nt) {
+            r.b = 0;
+            r.t = nt - 1 - idx;
+        }
+        return r;
+    }
     auto seq = [&](int b) { return one ? mine : prompt_seq(a, b); };
-    auto upto = [&](int w) {  // tiles with at most w chunks
+    int total = 0, lo = 0, hi = 0;
+    for (int b = lane; b < a.B; b += 32) {
+        const PromptSeq s = seq(b);
+        total += tiles_upto(s.n, s.p, T, d, INT_MAX / kWeightKeys);
+        if (s.n > 0) hi = max(hi, (s.p + s.n + kWeightKeys - 1) / kWeightKeys);
+    }
+    total = __reduce_add_sync(kFull, total);
+    hi = __reduce_max_sync(kFull, hi);
+    if (idx >= total) return r;
+    auto upto = [&](int w) {  // tiles of weight at most w
         int c = 0;
         for (int b = lane; b < a.B; b += 32) {
             const PromptSeq s = seq(b);
-            c += tiles_upto(s.n, s.p, T, w);
+            c += tiles_upto(s.n, s.p, T, d, w);
         }
         return __reduce_add_sync(kFull, c);
     };
-    total = upto(hi);
-    PromptTile r{-1, 0};
-    if (idx >= total) return r;
-    while (lo < hi) {  // the smallest w with at most idx tiles longer than w
+    while (lo < hi) {  // the smallest weight with at most idx heavier tiles
         const int mid = (lo + hi) >> 1;
         if (total - upto(mid) <= idx) hi = mid;
         else lo = mid + 1;
     }
-    int rank = idx - (total - upto(lo));  // among the tiles of lo chunks
+    int rank = idx - (total - upto(lo));  // among the tiles of this weight
     for (int b0 = 0; b0 < a.B; b0 += 32) {
         const int b = b0 + lane;
         int first = 0, cnt = 0;
+        PromptSeq s = mine;
         if (b < a.B) {
-            const PromptSeq s = seq(b);
-            first = tiles_upto(s.n, s.p, T, lo - 1);
-            cnt = tiles_upto(s.n, s.p, T, lo) - first;
+            s = seq(b);
+            first = tiles_upto(s.n, s.p, T, d, lo - 1);
+            cnt = tiles_upto(s.n, s.p, T, d, lo) - first;
         }
         int inc = cnt;
 #pragma unroll
@@ -107,11 +140,19 @@ __device__ inline PromptTile prompt_tile(const PromptArgs& a, int T, int idx) {
             const int src = __ffs(hit) - 1;
             r.b = b0 + src;
             r.t = __shfl_sync(kFull, first + rank - (inc - cnt), src);
+            from_lane(s, src);
             return r;
         }
         rank -= __shfl_sync(kFull, inc, 31);
     }
     return r;
+}
+
+// upper bound of the tiles of T tokens in a batch of at most N rows
+inline long prompt_tiles(int B, int N, int max_new, int T) {
+    const long per = (max_new + T - 1) / T;
+    const long packed = (long)N / T + (B < N ? B : N);
+    return per * B < packed ? per * B : packed;
 }
 
 // sign bits set where a half of w (two bf16) is infinite or NaN
@@ -122,13 +163,6 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
 // bf16 pair `w` with its non-finite halves (bits of `bad`) cleared
 __device__ __forceinline__ uint32_t clear2(uint32_t w, uint32_t bad) {
     return w & ~((bad >> 15) * 0xffffu);
-}
-
-// upper bound of the tiles of T tokens in a batch of at most N rows
-inline long prompt_tiles(int B, int N, int max_new, int T) {
-    const long per = (max_new + T - 1) / T;
-    const long packed = (long)N / T + (B < N ? B : N);
-    return per * B < packed ? per * B : packed;
 }
 
 // Partial results of key splits in the workspace: normalised fp32 rows

@@ -57,6 +57,7 @@ struct PromptTcArgs {
     PromptArgs p;
     SplitBuf buf;
     int G, T, page_rows;
+    FastDiv div_2T;
     float scale_log2;
     uint64_t wait_ns;
 };
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
     uint64_t* v_clean = o_last + 2;    // [kParts] V of the chunks that some row sees in part is cleared
     uint64_t* stagger = v_clean + kParts;  // tile 0's first softmax is done
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stagger + 1);
-    volatile int* s_tile = reinterpret_cast<volatile int*>(tmem_slot + 1);  // b, t, dirty
+    volatile int* s_tile = reinterpret_cast<volatile int*>(tmem_slot + 1);  // b, t, r0, n, p, dirty
 
     const PromptArgs& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -154,11 +155,14 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
         return;
     }
     if (warp == 0) {
-        const PromptTile t = prompt_tile(p, 2 * T, blockIdx.x / p.Hkv);
+        const PromptTile t = prompt_tile(p, 2 * T, a.div_2T, blockIdx.x / p.Hkv);
         if (lane == 0) {
             s_tile[0] = t.b;
             s_tile[1] = t.t;
-            s_tile[2] = 0;
+            s_tile[2] = t.s.r0;
+            s_tile[3] = t.s.n;
+            s_tile[4] = t.s.p;
+            s_tile[5] = 0;
         }
         if (blockIdx.x == 0 && split == 0)
             for (int b = lane; b < p.B; b += 32)
@@ -189,13 +193,15 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int b = s_tile[0];
-    const PromptSeq sq = prompt_seq(p, b < 0 ? 0 : b);
+    const struct {
+        int r0, n, p;
+    } sq = {s_tile[2], s_tile[3], s_tile[4]};
     const int tok0 = s_tile[1] * 2 * T;
     const int ntok = b < 0 ? 0 : min(2 * T, sq.n - tok0);
     const int pos0 = sq.p + tok0;                       // the first row's position
     const int keys = pos0 + ntok;                       // seen by the last row
     const int nch = b < 0 ? 0 : (keys + kPC - 1) / kPC;  // chunks of the longer tile
-    const int c0 = (int)((long)nch * split / C), c1 = (int)((long)nch * (split + 1) / C);
+    const int c0 = C == 1 ? 0 : nch * split / C, c1 = C == 1 ? nch : nch * (split + 1) / C;
     // chunks of each tile within this split
     auto count = [&](int tile) {
         const int n = min(T, ntok - tile * T);
@@ -382,7 +388,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                 const int i = 2 * j + 1, s = i % ST;
                 wait(&kv_full[s], (i / ST) & 1);
                 uint8_t* row = sKV + s * kTile + lr * 128;  // a thread per key
-#pragma unroll 2
+#pragma unroll 8
                 for (int x = 0; x < NSUB * 8; ++x) {
                     uint4* at = reinterpret_cast<uint4*>(row + (x >> 3) * kSub + ((x + lr) & 7) * 16);
                     if (key0 + lr >= keys) {  // no row sees this key: whatever is there
@@ -393,14 +399,14 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                     const uint32_t b0 = nonfinite2(w.x), b1 = nonfinite2(w.y), b2 = nonfinite2(w.z), b3 = nonfinite2(w.w);
                     if (b0 | b1 | b2 | b3) {
                         *at = make_uint4(clear2(w.x, b0), clear2(w.y, b1), clear2(w.z, b2), clear2(w.w, b3));
-                        s_tile[2] = 1;
+                        s_tile[5] = 1;
                     }
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&v_clean[c0 + j - (pos0 + 1) / kPC]);
             }
-            if (tile == 1 && j == 0 && cnt0 > 0) wait(stagger, 0);
+            if (tile == 1 && j == 0 && cnt0 > 2) wait(stagger, 0);  // (few chunks: no time to make up for it)
             wait(&s_full[tile], j & 1);
             tc_fence_after();
             uint32_t raw[kPC / 16][16];
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
             }
             // The clearing of a chunk precedes every product on it (of either
             // tile: v_clean), so a flag raised for this tile's chunks is visible here.
-            if (s_tile[2] && row_ok) {
+            if (s_tile[5] && row_ok) {
                 const int lo = max(c0 * kPC, (pos0 + 1) / kPC * kPC), hi = min(pos + 1, c1 * kPC);
                 for (int key = lo; key < hi; ++key) {
                     const __nv_bfloat16* vr;
@@ -522,25 +528,51 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                     }
                 }
             }
+            // Rows go through the tile's Q (every product on it is done), 256 bytes of
+            // each at a time, so that the warp's stores are whole rows: a store per
+            // thread into its own row would touch 32 lines each.
+            const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // a NaN sum stays NaN
+            const long row0 = (long)(sq.r0 + tok0 + tile * T) * p.Hq + g * G;  // of TMEM lane 0
             if (row_ok) {
-                const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // a NaN sum stays NaN
-                const long orow = (long)(sq.r0 + tok0 + tok) * p.Hq + g * G + lr % G;
-                if (C > 1) {
-                    const long prow = (long)split * p.N * p.Hq + orow;
-                    float4* dst = reinterpret_cast<float4*>(a.buf.o + prow * D);
-#pragma unroll
-                    for (int e = 0; e < D; e += 4)
-                        dst[e / 4] = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
-                    a.buf.lse2[prow] = l == 0.f ? -INFINITY : m + log2f(l);
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)p.out + orow * D);
-#pragma unroll
-                    for (int e = 0; e < D; e += 8)
-                        dst[e / 8] = make_uint4(p_pack(o[e] * inv, o[e + 1] * inv), p_pack(o[e + 2] * inv, o[e + 3] * inv),
-                                                p_pack(o[e + 4] * inv, o[e + 5] * inv),
-                                                p_pack(o[e + 6] * inv, o[e + 7] * inv));
-                    if (p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                const long orow = row0 + (long)(lr / G) * p.Hq + lr % G;
+                const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+                if (C > 1) a.buf.lse2[(long)split * p.N * p.Hq + orow] = lse2;
+                else if (p.lse) p.lse[orow] = lse2 * 0.69314718055994531f;
+            }
+            uint8_t* stage = sQ + tile * kQTile + (warp & 3) * 32 * (2 * D);  // 32 rows of 2 D bytes
+            constexpr int kRowVecs = 2 * D / 16;
+            auto put = [&](int x, uint4 v) {
+                *reinterpret_cast<uint4*>(stage + lane * (2 * D) + ((x ^ lane) & (kRowVecs - 1)) * 16) = v;
+            };
+            auto store = [&](uint8_t* base, long row_bytes, int off) {
+                __syncwarp();
+#pragma unroll 4
+                for (int x = lane; x < 32 * kRowVecs; x += 32) {
+                    const int r = x / kRowVecs, c = x % kRowVecs, q = (warp & 3) * 32 + r;
+                    if (q < T * G && tile * T + q / G < ntok)
+                        *reinterpret_cast<uint4*>(base + (row0 + (long)(q / G) * p.Hq + q % G) * row_bytes + off + c * 16) =
+                            *reinterpret_cast<const uint4*>(stage + r * (2 * D) + ((c ^ r) & (kRowVecs - 1)) * 16);
                 }
+                __syncwarp();
+            };
+            if (C > 1) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int x = 0; x < kRowVecs; ++x) {
+                        const int e = h * (D / 2) + 4 * x;
+                        put(x, make_uint4(__float_as_uint(o[e] * inv), __float_as_uint(o[e + 1] * inv),
+                                          __float_as_uint(o[e + 2] * inv), __float_as_uint(o[e + 3] * inv)));
+                    }
+                    store((uint8_t*)(a.buf.o + (long)split * p.N * p.Hq * D), D * 4, h * (2 * D));
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < kRowVecs; ++x)
+                    put(x, make_uint4(p_pack(o[8 * x] * inv, o[8 * x + 1] * inv), p_pack(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
+                                      p_pack(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
+                                      p_pack(o[8 * x + 6] * inv, o[8 * x + 7] * inv)));
+                store((uint8_t*)p.out, D * 2, 0);
             }
         }
     }
@@ -555,7 +587,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
 
 template <int D>
 constexpr size_t prompt_tc_smem() {
-    return (size_t)(2 * kPM + p_stages<D>() * kPC) * D * 2 + (2 + 2 * p_stages<D>() + 7 + 2 * kPParts + kParts) * 8 + 16;
+    return (size_t)(2 * kPM + p_stages<D>() * kPC) * D * 2 + (2 + 2 * p_stages<D>() + 7 + 2 * kPParts + kParts) * 8 + 32;
 }
 static_assert(prompt_tc_smem<128>() <= 232448 && prompt_tc_smem<64>() <= 232448, "shared memory of a CTA");
 
@@ -573,6 +605,7 @@ cudaError_t prompt_tc_launch(const PromptArgs& x, long tiles, int splits, const 
     const uint64_t D = x.D, Hq = x.Hq, Hkv = x.Hkv, N = x.N;
     a.G = x.Hq / x.Hkv;
     a.T = kPM / a.G;
+    a.div_2T = fast_div(2 * a.T);
     {
         const uint64_t dims[3] = {D, Hq, N}, strides[2] = {D * 2, (uint64_t)x.q_stride * 2};
         const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.T};
