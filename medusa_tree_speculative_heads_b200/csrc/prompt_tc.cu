@@ -57,7 +57,7 @@ struct PromptTcArgs {
     PromptArgs p;
     SplitBuf buf;
     int G, T, page_rows;
-    FastDiv div_2T;
+    FastDiv div_2T, div_G;
     float scale_log2;
     uint64_t wait_ns;
 };
@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
         // ---------------- softmax ----------------
         const int tile = warp >= 8 ? 1 : 0, cnt = tile ? cnt1 : cnt0;
         const int lr = (warp & 3) * 32 + lane;  // TMEM lane = row of the tile
-        const int tok = tile * T + lr / G;
+        const int row_tok = div_by(lr, a.div_G), row_head = lr - row_tok * G;
+        const int tok = tile * T + row_tok;
         const bool row_ok = lr < T * G && tok < ntok;
         const int pos = row_ok ? pos0 + tok : -1;  // a row of no token sees no key
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
             const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // a NaN sum stays NaN
             const long row0 = (long)(sq.r0 + tok0 + tile * T) * p.Hq + g * G;  // of TMEM lane 0
             if (row_ok) {
-                const long orow = row0 + (long)(lr / G) * p.Hq + lr % G;
+                const long orow = row0 + (long)row_tok * p.Hq + row_head;
                 const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
                 if (C > 1) a.buf.lse2[(long)split * p.N * p.Hq + orow] = lse2;
                 else if (p.lse) p.lse[orow] = lse2 * 0.69314718055994531f;
@@ -547,10 +548,12 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
             auto store = [&](uint8_t* base, long row_bytes, int off) {
                 __syncwarp();
 #pragma unroll 4
-                for (int x = lane; x < 32 * kRowVecs; x += 32) {
-                    const int r = x / kRowVecs, c = x % kRowVecs, q = (warp & 3) * 32 + r;
-                    if (q < T * G && tile * T + q / G < ntok)
-                        *reinterpret_cast<uint4*>(base + (row0 + (long)(q / G) * p.Hq + q % G) * row_bytes + off + c * 16) =
+                for (int x = 0; x < kRowVecs; ++x) {
+                    constexpr int kRows = 32 / kRowVecs;  // rows of a store
+                    const int r = x * kRows + lane / kRowVecs, c = lane % kRowVecs, q = (warp & 3) * 32 + r;
+                    const int t = div_by(q, a.div_G);
+                    if (t < T && tile * T + t < ntok)
+                        *reinterpret_cast<uint4*>(base + (row0 + (long)(t * p.Hq + q - t * G)) * row_bytes + off + c * 16) =
                             *reinterpret_cast<const uint4*>(stage + r * (2 * D) + ((c ^ r) & (kRowVecs - 1)) * 16);
                 }
                 __syncwarp();
@@ -606,6 +609,7 @@ cudaError_t prompt_tc_launch(const PromptArgs& x, long tiles, int splits, const 
     a.G = x.Hq / x.Hkv;
     a.T = kPM / a.G;
     a.div_2T = fast_div(2 * a.T);
+    a.div_G = fast_div(a.G);
     {
         const uint64_t dims[3] = {D, Hq, N}, strides[2] = {D * 2, (uint64_t)x.q_stride * 2};
         const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)a.T};
