@@ -648,11 +648,11 @@ int kv_page_plan(const int32_t* prefix_len, const int32_t* new_len, int B, int r
  *     pages[slot_map[t] / page_size, g, slot_map[t] % page_size, :] = rows[t, g, :]
  * k, v: rows of Hkv * D contiguous elements, k_stride and v_stride elements
  *   apart (>= Hkv * D and a multiple of 16 bytes: views into a fused
- *   projection's rows are taken as they are)
+ *   projection's rows are taken as they are); they may not overlap the pools
  * slot_map [N] int64: slots, distinct; -1 skips the row.  Other values
  *   outside [0, num_pages * page_size) are skipped too and set
  *   MEDUSA_STATUS_BAD_PAGE.
- * Limits: D in {64, 128}; N >= 0.
+ * Limits: D in {64, 128}; N >= 0; N * Hkv < 2^31; num_pages * page_size < 2^32.
  */
 int kv_append_paged(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int64_t* slot_map, int N,
                     void* k_pages, void* v_pages, int page_size, int num_pages, int Hkv, int D, medusa_dtype dt,

@@ -975,7 +975,8 @@ extern "C" int kv_append_paged(const void* k, const void* v, int64_t k_stride, i
     if (dt != MEDUSA_F32 && dt != MEDUSA_BF16) return fail(MEDUSA_ERR_UNSUPPORTED, "kv_append_paged: unknown dtype");
     if ((N != 0 && (!k || !v || !slot_map)) || !k_pages || !v_pages)
         return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_paged: NULL tensor argument");
-    if (N < 0 || page_size < 1 || num_pages < 1 || Hkv < 1 || Hkv > 1024)
+    if (N < 0 || page_size < 1 || num_pages < 1 || Hkv < 1 || Hkv > 1024 || (long)N * Hkv >= (1L << 31) ||
+        (long)num_pages * page_size >= (1L << 32))
         return fail(MEDUSA_ERR_INVALID_ARG, "kv_append_paged: bad sizes N=%d page_size=%d num_pages=%d Hkv=%d", N,
                     page_size, num_pages, Hkv);
     if (D != 64 && D != 128) return fail(MEDUSA_ERR_UNSUPPORTED, "kv_append_paged: head_dim %d (64 or 128)", D);
