@@ -155,6 +155,17 @@ inline long prompt_tiles(int B, int N, int max_new, int T) {
     return per * B < packed ? per * B : packed;
 }
 
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // sign bits set where a half of w (two bf16) is infinite or NaN
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
     return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;

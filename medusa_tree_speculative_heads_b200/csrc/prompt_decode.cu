@@ -255,18 +255,18 @@ __global__ void __launch_bounds__(kDThreads, kDCtasPerSm) decode_kernel(const __
     bool ok = true;
     if (warp == 0) {
         // ---------------- producer ----------------
-        // A lane's box: page_rows keys of 64 elements of K or of V.  The box of
-        // the chunk after the one being issued is looked up meanwhile, across
-        // pairs too.
+        // A lane looks up a box of page_rows keys; the boxes of the chunk after the
+        // one being issued are looked up meanwhile, across pairs too.  The warp
+        // runs converged and one elected lane issues (a copy per lane goes through
+        // the lanes one after the other, some 100 cycles each).
         const int pr = a.page_rows, nbox = kDC / pr;
-        const int box = lane % nbox, part = lane / nbox, sub = part % NSUB, kv = part / NSUB;
-        const bool mine = part < 2 * NSUB;
+        const bool lead = elect_one();
         int c = more ? walk.c_lo : 0;
         auto look_up = [&](int& y, int& z) {  // (row in the page, page * Hkv + kv-head), z < 0: not loaded
-            const int pos = c * kDC + box * pr;
+            const int pos = c * kDC + lane * pr;
             y = 0;
             z = -1;
-            if (!mine || pos >= walk.pos + walk.n) return;
+            if (lane >= nbox || pos >= walk.pos + walk.n) return;
             const int page = p.block_table[(long)walk.b * p.max_pages + pos / p.page_size];
             if (page < 0 || page >= p.num_pages) {
                 set_status(p.status, MEDUSA_STATUS_BAD_PAGE);
@@ -296,12 +296,13 @@ __global__ void __launch_bounds__(kDThreads, kDCtasPerSm) decode_kernel(const __
                     ok = false;
                     break;
                 }
-                if (lane == 0) {
+                if (lead) {
                     mbar_arrive_expect_tx(&sm.q_full[qs], (uint32_t)(kDR / G * G * 128 * NSUB));
 #pragma unroll
                     for (int x = 0; x < NSUB; ++x)
                         tma_load_3d(sm.q[qs] + x * kDR * 128, &a.mq, x * 64, qhead, qrow, &sm.q_full[qs]);
                 }
+                __syncwarp();
                 ++seg;
             }
             const unsigned loads = __ballot_sync(kFull, cz >= 0);
@@ -309,11 +310,18 @@ __global__ void __launch_bounds__(kDThreads, kDCtasPerSm) decode_kernel(const __
                 ok = false;
                 break;
             }
-            if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(__popc(loads) * pr * 128));
-            __syncwarp();
-            if (cz >= 0)
-                tma_load_3d(sm.ring[s][kv] + sub * kSub + box * pr * 128, kv ? &a.mv : &a.mk, sub * 64, cy, cz,
-                            &sm.full[s]);
+            if (lead) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(__popc(loads) * 2 * NSUB * pr * 128));
+            for (int x = 0; x < nbox; ++x) {
+                const int by = __shfl_sync(kFull, cy, x), bz = __shfl_sync(kFull, cz, x);
+                if (bz < 0) continue;
+                if (lead) {
+#pragma unroll
+                    for (int u = 0; u < 2 * NSUB; ++u)
+                        tma_load_3d(sm.ring[s][u / NSUB] + (u % NSUB) * kSub + x * pr * 128, u < NSUB ? &a.mk : &a.mv,
+                                    (u % NSUB) * 64, by, bz, &sm.full[s]);
+                }
+                __syncwarp();
+            }
             ++it;
         }
         if (!ok && lane == 0) set_status(p.status, MEDUSA_STATUS_TIMEOUT);

@@ -18,7 +18,7 @@
 // the next chunk; when the sum of a part of the chunk exceeds 2^32 (or is not a
 // number) the chunk's maximum is taken after all, m raised at once, and the
 // part's weights are computed again.
-// Warps: 0 producer (TMA), 1 and 2 MMA issue of tiles 0 and 1 (1 also TMEM
+// Warps: 0 and 3 producers (TMA: Q and K, V), 1 and 2 MMA issue of tiles 0 and 1 (1 also TMEM
 // allocation), 4-7 softmax of tile 0, 8-11 of tile 1.  All 512 TMEM columns
 // are in use (2 x 128 of S, 2 x 128 of O), so a tile alternates between its
 // softmax and its products; tile 1 starts a softmax later, so that one tile's
@@ -42,7 +42,7 @@ namespace medusa {
 
 namespace {
 
-constexpr int kPW = 12;    // warps: 0 producer, 1 and 2 MMA, 4-11 softmax
+constexpr int kPW = 12;    // warps: 0 and 3 producers, 1 and 2 MMA, 4-11 softmax
 constexpr int kPM = 128;   // rows of a query tile
 constexpr int kParts = 3;  // most chunks that some row of a CTA sees in part: its 256 tokens and a first chunk
 constexpr int kPC = 128;   // keys per chunk
@@ -94,17 +94,6 @@ __device__ __forceinline__ uint32_t p_pack(float lo, float hi) {
 
 // a condition whose code belongs out of the way of the hot path
 __device__ __forceinline__ bool rare(bool x) { return __builtin_expect(x, 0); }
-
-// true in one lane of the (converged) warp
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(p));
-    return p != 0;
-}
 
 // MN-major operand as TMA writes a (64 MN x rows K) box with a 128-byte
 // swizzle: 8 K-rows of 128 bytes per 1024-byte group; `lbo`: byte distance to
@@ -223,62 +212,79 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
     // Registers: 384 threads are launched with 168 each; the softmax warps take
     // the others' share (88 + 2 * 208 = 3 * 168).
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 0) {
-        // ---------------- producer ----------------
+    if (warp == 0 || warp == 3) {
+        // ---------------- producers: K (and Q), V ----------------
+        // Like the MMA warps these run converged and one elected lane issues: a
+        // copy per lane goes through the lanes one after the other, some 100
+        // cycles each, and 16-row pages make 16 copies of a chunk of K.
         if (cmax > 0) {
-            if (lane == 0) {
+            const bool lead = elect_one();
+            const int kv = warp == 3;
+            if (kv == 0) {
 #pragma unroll
                 for (int tile = 0; tile < 2; ++tile) {
-                    if ((tile == 0 ? cnt0 : cnt1) == 0) continue;
+                    if ((tile == 0 ? cnt0 : cnt1) == 0 || !lead) continue;
                     mbar_arrive_expect_tx(&q_full[tile], (uint32_t)(T * G * 128 * NSUB));
 #pragma unroll
                     for (int sub = 0; sub < NSUB; ++sub)
                         tma_load_3d(sQ + tile * kQTile + sub * kQSub, &a.mq, sub * 64, g * G, sq.r0 + tok0 + tile * T,
                                     &q_full[tile]);
                 }
+                __syncwarp();
             }
-            // the lane's box of a chunk: 64 elements of page_rows (packed: all 128) keys
+            // a chunk's boxes of page_rows (packed: all 128) keys; a lane looks one up
             const int pr = paged ? a.page_rows : kPC, nbox = kPC / pr;
-            const int box = lane / NSUB, sub = lane % NSUB;
-            const bool mine = box < nbox;
-            auto page_of = [&](int j) -> int {  // of the lane's box in chunk j; -1: not loaded
-                const int pos = (c0 + j) * kPC + box * pr;
-                if (!mine || j >= cmax || pos >= keys) return -1;
-                if (!paged) return 0;
+            const CUtensorMap* map = kv ? &a.mv : &a.mk;
+            // (row in the page or packed row, page * Hkv + kv-head or kv-head); z < 0: not loaded
+            auto look_up = [&](int j, int& y, int& z) {
+                const int pos = (c0 + j) * kPC + lane * pr;
+                y = 0;
+                z = -1;
+                if (lane >= nbox || j >= cmax || pos >= keys) return;
+                if (!paged) {
+                    y = sq.r0 + pos;
+                    z = g;
+                    return;
+                }
                 const int page = p.block_table[(long)b * p.max_pages + pos / p.page_size];
-                if (page >= 0 && page < p.num_pages) return page;
-                set_status(p.status, MEDUSA_STATUS_BAD_PAGE);
-                return -1;
+                if (page >= 0 && page < p.num_pages) {
+                    y = pos % p.page_size;
+                    z = page * p.Hkv + g;
+                } else {
+                    set_status(p.status, MEDUSA_STATUS_BAD_PAGE);
+                }
             };
-            int next = page_of(0), issued = 0;
-            for (int j = 0; j < cmax && ok; ++j) {
-                const int page = next;
-                next = page_of(j + 1);  // one chunk ahead: in flight during this chunk's waits
-                const unsigned loads = __ballot_sync(kFull, page >= 0);
-                const int pos = (c0 + j) * kPC + box * pr;
+            int next_y, next_z, issued = 0;
+            look_up(0, next_y, next_z);
+            for (int j = 0; j < cmax; ++j) {
+                const int y = next_y, z = next_z, i = 2 * j + kv, s = i % ST;
+                look_up(j + 1, next_y, next_z);  // one chunk ahead: in flight during this chunk's wait
+                const unsigned loads = __ballot_sync(kFull, z >= 0);
+                if (i >= ST && !__all_sync(kFull, mbar_wait(&kv_empty[s], ((i / ST) - 1) & 1, wait_ns))) {
+                    if (lane == 0) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
+                    break;
+                }
+                if (lead) mbar_arrive_expect_tx(&kv_full[s], (uint32_t)(__popc(loads) * NSUB * pr * 128));
+                ++issued;
+                for (int x = 0; x < nbox; ++x) {
+                    const int by = __shfl_sync(kFull, y, x), bz = __shfl_sync(kFull, z, x);
+                    if (bz < 0) continue;
+                    if (lead) {
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int i = 2 * j + kv, s = i % ST;
-                    if (i >= ST && !__all_sync(kFull, mbar_wait(&kv_empty[s], ((i / ST) - 1) & 1, wait_ns))) {
-                        ok = false;
-                        break;
+                        for (int sub = 0; sub < NSUB; ++sub)
+                            tma_load_3d(sKV + s * kTile + sub * kSub + x * pr * 128, map, sub * 64,
+                                        paged ? by : bz, paged ? bz : by, &kv_full[s]);
                     }
-                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[s], (uint32_t)(__popc(loads) * pr * 128));
                     __syncwarp();
-                    ++issued;
-                    if (page >= 0) {
-                        uint8_t* dst = sKV + s * kTile + sub * kSub + box * pr * 128;
-                        const CUtensorMap* m = kv ? &a.mv : &a.mk;
-                        if (paged) tma_load_3d(dst, m, sub * 64, pos % p.page_size, page * p.Hkv + g, &kv_full[s]);
-                        else tma_load_3d(dst, m, sub * 64, g, sq.r0 + pos, &kv_full[s]);
-                    }
                 }
             }
-            if (!ok && lane == 0) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
             // drain: no copy may still be landing when the CTA exits
-            if (cnt0 > 0) mbar_wait(&q_full[0], 0);
-            if (cnt1 > 0) mbar_wait(&q_full[1], 0);
-            for (int i = max(0, issued - ST); i < issued; ++i) mbar_wait(&kv_full[i % ST], (i / ST) & 1);
+            if (kv == 0 && cnt0 > 0) mbar_wait(&q_full[0], 0);
+            if (kv == 0 && cnt1 > 0) mbar_wait(&q_full[1], 0);
+            for (int j = max(0, issued - (ST + 1) / 2); j < issued; ++j) {
+                const int i = 2 * j + kv;  // (a stage that the other producer has used since had landed)
+                if (i + ST >= 2 * issued) mbar_wait(&kv_full[i % ST], (i / ST) & 1);
+            }
         }
     } else if (warp < 3) {
         // ---------------- MMA issuer of a tile ----------------
