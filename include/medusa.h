@@ -636,7 +636,7 @@ int kv_commit_paged(void* k_pages, void* v_pages, const void* k_tree, const void
  * entry and slots become -1).
  * The calls that use one pool are ordered by the caller: two plans on the
  * same state may not overlap.
- * Limits: B <= 8192; max_tokens >= 1.
+ * Limits: B <= 8192; 1 <= max_tokens <= 2^30.
  */
 int kv_page_plan(const int32_t* prefix_len, const int32_t* new_len, int B, int room, int32_t* block_table,
                  int max_pages, int page_size, int num_pages, const int32_t* owned, int32_t* owned_out,
@@ -667,7 +667,8 @@ int kv_append_paged(const void* k, const void* v, int64_t k_stride, int64_t v_st
  *   v_stride elements apart (multiples of 16 bytes; heads contiguous)
  * max_len: an upper bound of the sequences' lengths (0: N).  A longer one, or
  *   row starts that fall or leave [0, N], set MEDUSA_STATUS_BAD_LENGTH; the
- *   rows past the bound are not computed.
+ *   rows past the bound are not computed, and those of sequences with such
+ *   starts mean nothing.
  * scale: softmax scale; <= 0 means 1/sqrt(D)
  * out [N, Hq, D] dtype dt (contiguous); lse [N, Hq] f32, nullable: natural
  *   log-sum-exp of the scaled scores
@@ -700,9 +701,9 @@ int prompt_attention(const void* q, const void* k, const void* v, int64_t q_stri
  *   clamped.  A needed table entry outside [0, num_pages) sets
  *   MEDUSA_STATUS_BAD_PAGE; that sequence's output is then not meaningful.
  * Slots at or past the last new token may hold anything.
- * Limits as prompt_attention; any page_size >= 1 (bf16: the tensor-core
- * kernels read sizes of 8, 16, 32 and multiples of 64; others run on CUDA
- * cores).
+ * Limits as prompt_attention; num_pages * Hkv < 2^31; any page_size >= 1
+ * (bf16: the tensor-core kernels read sizes of 8, 16, 32 and multiples of 64;
+ * others run on CUDA cores).
  * Workspace: chunk_attention_paged_workspace_size(...) bytes.
  */
 size_t chunk_attention_paged_workspace_size(int B, int N, int max_new, int max_prefix, int max_pages, int page_size,

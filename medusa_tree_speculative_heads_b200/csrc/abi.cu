@@ -932,7 +932,7 @@ extern "C" int kv_page_plan(const int32_t* prefix_len, const int32_t* new_len, i
         !free_count_out || !row_start || !slot_map)
         return fail(MEDUSA_ERR_INVALID_ARG, "kv_page_plan: NULL tensor argument");
     if (B < 1 || room < 0 || max_pages < 1 || page_size < 1 || num_pages < 1 || max_tokens < 1 ||
-        (long)max_pages * page_size > (1L << 30))
+        max_tokens > (1 << 30) || (long)max_pages * page_size > (1L << 30))
         return fail(MEDUSA_ERR_INVALID_ARG,
                     "kv_page_plan: bad sizes B=%d room=%d max_pages=%d page_size=%d num_pages=%d max_tokens=%d", B,
                     room, max_pages, page_size, num_pages, max_tokens);
@@ -1102,9 +1102,11 @@ extern "C" int chunk_attention_paged(const void* q, int64_t q_stride, const void
                                      medusa_stream_t stream) {
     if (!block_table || !prefix_len)
         return fail(MEDUSA_ERR_INVALID_ARG, "chunk_attention_paged: NULL tensor argument");
-    if (max_pages < 1 || page_size < 1 || num_pages < 1 || (long)max_pages * page_size > (1L << 30))
-        return fail(MEDUSA_ERR_INVALID_ARG, "chunk_attention_paged: bad sizes max_pages=%d page_size=%d num_pages=%d",
-                    max_pages, page_size, num_pages);
+    if (max_pages < 1 || page_size < 1 || num_pages < 1 || (long)max_pages * page_size > (1L << 30) || Hkv < 1 ||
+        (long)num_pages * Hkv >= (1L << 31))
+        return fail(MEDUSA_ERR_INVALID_ARG,
+                    "chunk_attention_paged: bad sizes max_pages=%d page_size=%d num_pages=%d Hkv=%d", max_pages,
+                    page_size, num_pages, Hkv);
     const int cap = max_pages * page_size;
     if (max_prefix <= 0) max_prefix = cap;
     if (max_prefix > cap)

@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendArgs a) {
             if (slot != -1) bad = MEDUSA_STATUS_BAD_PAGE;
             continue;
         }
-        const uint32_t page = (uint32_t)slot / (uint32_t)a.page_size, off = (uint32_t)slot - page * (uint32_t)a.page_size;
+        const uint32_t page = (uint32_t)slot / (uint32_t)a.page_size;
+        const uint32_t off = (uint32_t)slot - page * (uint32_t)a.page_size;
         dst[j] = (((long)page * a.Hkv + (long)g) * a.page_size + (long)off) * (kVecs * 16) + c * 16;
         const long src = (long)g * (kVecs * 16) + c * 16;
         kr[j] = ld_nc(k + (long)t * a.k_stride + src);

@@ -155,6 +155,18 @@ inline long prompt_tiles(int B, int N, int max_new, int T) {
     return per * B < packed ? per * B : packed;
 }
 
+// 2^x on the SFU (relative error about 2^-22; 2^-inf = 0)
+__device__ __forceinline__ float exp2_sfu(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
 // true in one lane of the (converged) warp
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;

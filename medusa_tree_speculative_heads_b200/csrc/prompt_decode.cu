@@ -154,15 +154,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float d_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t d_pack(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
 // barrier of the consumer warps
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kDW * 32) : "memory"); }
 
@@ -398,10 +389,11 @@ __global__ void __launch_bounds__(kDThreads, kDCtasPerSm) decode_kernel(const __
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = h ? r1 : r0;
-                const float top = fmaxf(fmaxf(sm.mx[0][r], sm.mx[1][r]), fmaxf(sm.mx[2][r], sm.mx[3][r])) * a.scale_log2;
+                const float top =
+                    fmaxf(fmaxf(sm.mx[0][r], sm.mx[1][r]), fmaxf(sm.mx[2][r], sm.mx[3][r])) * a.scale_log2;
                 al[h] = 1.f;
                 if (top > m[h] + 8.f) {  // a new reference only when the maximum rises by more than 2^8
-                    al[h] = d_exp2(m[h] - top);
+                    al[h] = exp2_sfu(m[h] - top);
                     m[h] = top;
                     raised = true;
                 }
@@ -413,12 +405,12 @@ __global__ void __launch_bounds__(kDThreads, kDCtasPerSm) decode_kernel(const __
                 float pv[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    pv[e] = d_exp2(fmaf(sc[n][e], a.scale_log2, e < 2 ? -mu0 : -mu1));
+                    pv[e] = exp2_sfu(fmaf(sc[n][e], a.scale_log2, e < 2 ? -mu0 : -mu1));
                     rs[e >> 1] += pv[e];
                 }
                 const int col = (w * 16 + 8 * n + 2 * cc) * 2;
-                *reinterpret_cast<uint32_t*>(sm.p + r0 * kPStride + col) = d_pack(pv[0], pv[1]);
-                *reinterpret_cast<uint32_t*>(sm.p + r1 * kPStride + col) = d_pack(pv[2], pv[3]);
+                *reinterpret_cast<uint32_t*>(sm.p + r0 * kPStride + col) = pack_bf16(pv[0], pv[1]);
+                *reinterpret_cast<uint32_t*>(sm.p + r1 * kPStride + col) = pack_bf16(pv[2], pv[3]);
             }
             l[0] = l[0] * al[0] + rs[0];
             l[1] = l[1] * al[1] + rs[1];
@@ -441,7 +433,8 @@ __global__ void __launch_bounds__(kDThreads, kDCtasPerSm) decode_kernel(const __
                     const int row = e / (NSUB * 8), x = e % (NSUB * 8);
                     uint4* at = reinterpret_cast<uint4*>(vt + (x >> 3) * kSub + row * 128 + (x & 7) * 16);
                     const uint4 v = *at;
-                    const uint32_t b0 = nonfinite2(v.x), b1 = nonfinite2(v.y), b2 = nonfinite2(v.z), b3 = nonfinite2(v.w);
+                    const uint32_t b0 = nonfinite2(v.x), b1 = nonfinite2(v.y);
+                    const uint32_t b2 = nonfinite2(v.z), b3 = nonfinite2(v.w);
                     if (key0 + row >= keys) {
                         *at = make_uint4(0u, 0u, 0u, 0u);
                     } else if (b0 | b1 | b2 | b3) {
@@ -509,7 +502,7 @@ __global__ void __launch_bounds__(kDThreads, kDCtasPerSm) decode_kernel(const __
                 __nv_bfloat16* dst = (__nv_bfloat16*)p.out + orow * D + w * NT * 8 + 2 * cc;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    *reinterpret_cast<uint32_t*>(dst + n * 8) = d_pack(o[n][2 * h] * inv, o[n][2 * h + 1] * inv);
+                    *reinterpret_cast<uint32_t*>(dst + n * 8) = pack_bf16(o[n][2 * h] * inv, o[n][2 * h + 1] * inv);
                 if (p.lse && w == 0 && cc == 0)
                     p.lse[orow] = L == 0.f ? -INFINITY : (m[h] + log2f(L)) * 0.69314718055994531f;
             } else {
@@ -529,7 +522,8 @@ __global__ void __launch_bounds__(kDThreads, kDCtasPerSm) decode_kernel(const __
 // the four sums are added in order.
 constexpr int kMergeWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __grid_constant__ DecodeArgs a, int grid) {
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    decode_merge_kernel(const __grid_constant__ DecodeArgs a, int grid) {
     constexpr int PL = D / 32;
     __shared__ float s_acc[kMergeWarps][D], s_w[kMergeWarps];
     const PromptArgs& p = a.p;
@@ -555,7 +549,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const __
     for (int e = 0; e < PL; ++e) acc[e] = 0.f;
 #pragma unroll 4
     for (int i = first + warp; i <= last; i += kMergeWarps) {
-        const float w = d_exp2(a.part_lse2[slot(i)] - mu);
+        const float w = exp2_sfu(a.part_lse2[slot(i)] - mu);
         const float* src = a.part_o + slot(i) * D + lane * PL;
         wsum += w;
 #pragma unroll
@@ -631,7 +625,8 @@ cudaError_t decode_launch(const PromptArgs& x, cudaStream_t st) {
     a.scale_log2 = x.scale * 1.4426950408889634f;
     a.wait_ns = wait_limit_ns();
     // a CTA per run, two per SM, but no more runs than there can be chunks
-    const long units = (long)(x.B < x.N ? x.B : x.N) * x.Hkv * (((long)x.max_prefix + x.max_new + kDC - 1) / kDC + kPairCost);
+    const long chunks = ((long)x.max_prefix + x.max_new + kDC - 1) / kDC;
+    const long units = (long)(x.B < x.N ? x.B : x.N) * x.Hkv * (chunks + kPairCost);
     const long most = (long)kDCtasPerSm * num_sms();
     const int runs = (int)(units < most ? (units < 1 ? 1 : units) : most);
     a.part_o = (float*)x.ws;

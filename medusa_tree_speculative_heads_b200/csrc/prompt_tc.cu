@@ -12,22 +12,38 @@
 // with the reference m and the sum l of each row in the fp32 registers of its
 // softmax thread.  P is rounded to bf16 (2^-8 relative, as the operands are);
 // l sums it unrounded.
+//
 // Any m gives the same result as long as nothing overflows, so no maximum is
 // taken after the first chunk: the sum of a chunk's weights bounds them.  When
 // it exceeds 2^8, m is raised by its logarithm, and O in TMEM rescaled, before
 // the next chunk; when the sum of a part of the chunk exceeds 2^32 (or is not a
 // number) the chunk's maximum is taken after all, m raised at once, and the
-// part's weights are computed again.
-// Warps: 0 and 3 producers (TMA: Q and K, V), 1 and 2 MMA issue of tiles 0 and 1 (1 also TMEM
-// allocation), 4-7 softmax of tile 0, 8-11 of tile 1.  All 512 TMEM columns
-// are in use (2 x 128 of S, 2 x 128 of O), so a tile alternates between its
-// softmax and its products; tile 1 starts a softmax later, so that one tile's
-// softmax runs beside the other's products.  P is handed over in kPParts parts,
-// so that PV runs while the last exponentials are taken.
-// A chunk costs each tile 2 x 512 tensor cycles (D = 128) and 128 x 128
-// exponentials, 1024 cycles of the SM's 16 per clock; what bounds the kernel
-// is the alternation: a tile's softmax (one warp per scheduler) and then two
-// chains of eight products, with a hand-over of some 200 cycles each way.
+// part's weights are computed again.  (Taking the maximum of 128 scores first
+// cost 400 of a chunk's 4200 cycles.)
+//
+// Warps: 0 and 3 producers (TMA: Q and K, V), 1 and 2 MMA issue of tiles 0 and
+// 1 (1 also TMEM allocation), 4-7 softmax of tile 0, 8-11 of tile 1.  All 512
+// TMEM columns are in use (2 x 128 of S, 2 x 128 of O), so a tile alternates
+// between its softmax and its products; tile 1 starts a softmax later, so that
+// one tile's softmax runs beside the other's products (both in step: 15%
+// slower).  P is handed over in two parts, so that PV runs while the last
+// exponentials are taken.  64-key chunks with two S buffers let QK run ahead,
+// but a product with N = 64 takes 50 cycles against 64 with N = 128 (its A
+// operand costs the same shared-memory reads), and the kernel came out no
+// faster; two threads per row, turns at the exponentials, and a polynomial on
+// the FMA pipe for a part of them (22 cycles a value of a warp, the SFU's 8)
+// were all slower.
+//
+// Bound: a chunk costs each tile 2 x 512 tensor cycles (D = 128) and 128 x 128
+// exponentials, 1024 cycles of the SM's 16 per clock.  One tile alone takes
+// 3300 cycles a chunk (softmax 1650, products 1024, two hand-overs of some 200
+// to 300), both together 4300: each slows the other's exponentials and
+// products.  One prompt of 32768 tokens, 32/8 heads of 128: 7.9 to 8.3 ms, 1.06
+// to 1.12 PFLOP/s (7.05 ms, 1.25 PFLOP/s, before the clock drops under the
+// power cap); 2048 tokens 46.5 us, of which the prologue (tile lookup, the
+// first K) and the epilogue are some 6 us for each of the up to two CTAs of an
+// SM.
+//
 // The visible keys of a row are 0 .. its position, so only the chunks that
 // reach past the tile's first position need a mask.  In those, V elements
 // that are not finite are cleared in shared memory (0 * NaN must not reach a
@@ -62,12 +78,6 @@ struct PromptTcArgs {
     uint64_t wait_ns;
 };
 
-__device__ __forceinline__ float p_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // two fp32 values in one 64-bit register: the FMA pipe takes both at once
 __device__ __forceinline__ uint64_t f2(float x, float y) {
     uint64_t r;
@@ -87,11 +97,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t p_pack(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-
 // a condition whose code belongs out of the way of the hot path
 __device__ __forceinline__ bool rare(bool x) { return __builtin_expect(x, 0); }
 
@@ -205,156 +210,158 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
     // barrier still meets its threads.  Each lane polls for itself.
     bool ok = true;
     auto wait = [&](uint64_t* bar, int parity) {
-        if (rare(ok && !mbar_try_wait(bar, parity))) ok = mbar_wait(bar, parity, wait_ns);
+        if (rare(ok && (kTestWaits || !mbar_try_wait(bar, parity)))) ok = mbar_wait(bar, parity, wait_ns);
         __syncwarp();
     };
     if (warp < 4) {
-    // Registers: 384 threads are launched with 168 each; the softmax warps take
-    // the others' share (88 + 2 * 208 = 3 * 168).
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 0 || warp == 3) {
-        // ---------------- producers: K (and Q), V ----------------
-        // Like the MMA warps these run converged and one elected lane issues: a
-        // copy per lane goes through the lanes one after the other, some 100
-        // cycles each, and 16-row pages make 16 copies of a chunk of K.
-        if (cmax > 0) {
-            const bool lead = elect_one();
-            const int kv = warp == 3;
-            if (kv == 0) {
+        // Registers: 384 threads are launched with 168 each; the softmax warps take
+        // the others' share (88 + 2 * 208 = 3 * 168).
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 0 || warp == 3) {
+            // ---------------- producers: K (and Q), V ----------------
+            // Like the MMA warps these run converged and one elected lane issues: a
+            // copy per lane goes through the lanes one after the other, some 100
+            // cycles each, and 16-row pages make 16 copies of a chunk of K.
+            if (cmax > 0) {
+                const bool lead = elect_one();
+                const int kv = warp == 3;
+                if (kv == 0) {
 #pragma unroll
-                for (int tile = 0; tile < 2; ++tile) {
-                    if ((tile == 0 ? cnt0 : cnt1) == 0 || !lead) continue;
-                    mbar_arrive_expect_tx(&q_full[tile], (uint32_t)(T * G * 128 * NSUB));
-#pragma unroll
-                    for (int sub = 0; sub < NSUB; ++sub)
-                        tma_load_3d(sQ + tile * kQTile + sub * kQSub, &a.mq, sub * 64, g * G, sq.r0 + tok0 + tile * T,
-                                    &q_full[tile]);
-                }
-                __syncwarp();
-            }
-            // a chunk's boxes of page_rows (packed: all 128) keys; a lane looks one up
-            const int pr = paged ? a.page_rows : kPC, nbox = kPC / pr;
-            const CUtensorMap* map = kv ? &a.mv : &a.mk;
-            // (row in the page or packed row, page * Hkv + kv-head or kv-head); z < 0: not loaded
-            auto look_up = [&](int j, int& y, int& z) {
-                const int pos = (c0 + j) * kPC + lane * pr;
-                y = 0;
-                z = -1;
-                if (lane >= nbox || j >= cmax || pos >= keys) return;
-                if (!paged) {
-                    y = sq.r0 + pos;
-                    z = g;
-                    return;
-                }
-                const int page = p.block_table[(long)b * p.max_pages + pos / p.page_size];
-                if (page >= 0 && page < p.num_pages) {
-                    y = pos % p.page_size;
-                    z = page * p.Hkv + g;
-                } else {
-                    set_status(p.status, MEDUSA_STATUS_BAD_PAGE);
-                }
-            };
-            int next_y, next_z, issued = 0;
-            look_up(0, next_y, next_z);
-            for (int j = 0; j < cmax; ++j) {
-                const int y = next_y, z = next_z, i = 2 * j + kv, s = i % ST;
-                look_up(j + 1, next_y, next_z);  // one chunk ahead: in flight during this chunk's wait
-                const unsigned loads = __ballot_sync(kFull, z >= 0);
-                if (i >= ST && !__all_sync(kFull, mbar_wait(&kv_empty[s], ((i / ST) - 1) & 1, wait_ns))) {
-                    if (lane == 0) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
-                    break;
-                }
-                if (lead) mbar_arrive_expect_tx(&kv_full[s], (uint32_t)(__popc(loads) * NSUB * pr * 128));
-                ++issued;
-                for (int x = 0; x < nbox; ++x) {
-                    const int by = __shfl_sync(kFull, y, x), bz = __shfl_sync(kFull, z, x);
-                    if (bz < 0) continue;
-                    if (lead) {
+                    for (int tile = 0; tile < 2; ++tile) {
+                        if ((tile == 0 ? cnt0 : cnt1) == 0 || !lead) continue;
+                        mbar_arrive_expect_tx(&q_full[tile], (uint32_t)(T * G * 128 * NSUB));
 #pragma unroll
                         for (int sub = 0; sub < NSUB; ++sub)
-                            tma_load_3d(sKV + s * kTile + sub * kSub + x * pr * 128, map, sub * 64,
-                                        paged ? by : bz, paged ? bz : by, &kv_full[s]);
+                            tma_load_3d(sQ + tile * kQTile + sub * kQSub, &a.mq, sub * 64, g * G,
+                                        sq.r0 + tok0 + tile * T, &q_full[tile]);
                     }
                     __syncwarp();
                 }
-            }
-            // drain: no copy may still be landing when the CTA exits
-            if (kv == 0 && cnt0 > 0) mbar_wait(&q_full[0], 0);
-            if (kv == 0 && cnt1 > 0) mbar_wait(&q_full[1], 0);
-            for (int j = max(0, issued - (ST + 1) / 2); j < issued; ++j) {
-                const int i = 2 * j + kv;  // (a stage that the other producer has used since had landed)
-                if (i + ST >= 2 * issued) mbar_wait(&kv_full[i % ST], (i / ST) & 1);
-            }
-        }
-    } else if (warp < 3) {
-        // ---------------- MMA issuer of a tile ----------------
-        // A warp per tile, so that the waits of one do not hold up the other's
-        // products.  The whole warp runs the loop, so that descriptors and
-        // addresses stay in uniform registers; one elected lane issues.
-        const int tile = warp - 1;
-        const int n = __shfl_sync(kFull, tile ? cnt1 : cnt0, 0), other = __shfl_sync(kFull, tile ? cnt0 : cnt1, 0);
-        if (n > 0) {
-            const bool lead = elect_one();
-            const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-            // a stage is free after one arrival for each tile (two of the only one that uses it)
-            auto release = [&](int s, int j) {
-                tc_commit(&kv_empty[s]);
-                if (j >= other) tc_commit(&kv_empty[s]);
-            };
-            const uint64_t qd = sw128_kmajor_desc(smem_addr(sQ) + tile * kQTile), kd = sw128_kmajor_desc(smem_addr(sKV));
-            const uint64_t vd = p_mnmajor_desc(smem_addr(sKV), kSub);
-            const uint32_t t_s = tm + tile * kPC, t_o = tm + 256 + tile * 128;
-            auto issue_qk = [&](int j) {
-                const int i = 2 * j, s = i % ST;
-                wait(&kv_full[s], (i / ST) & 1);
-                tc_fence_after();
-                if (lead) {
-#pragma unroll
-                    for (int sub = 0; sub < NSUB; ++sub)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            tc_mma_bf16(t_s, qd + (uint64_t)((sub * kQSub) >> 4) + 2 * ks,
-                                        kd + (uint64_t)((s * kTile + sub * kSub) >> 4) + 2 * ks, kIdescQK, (sub | ks) != 0);
-                    // completes after this tile's products so far: its last PV too
-                    tc_commit(&s_full[tile]);
-                    release(s, j);
-                }
-                __syncwarp();
-            };
-            wait(&q_full[tile], 0);
-            issue_qk(0);
-            for (int j = 0; j < n; ++j) {
-                const int i = 2 * j + 1, s = i % ST;
-                const uint64_t bd = vd + (uint64_t)((s * kTile) >> 4);
-                auto pv = [&](int ks) {  // 16 keys: 8 columns of P, two 1024-byte groups of V
-                    tc_mma_bf16_ts(t_o, t_s + ks * 8, bd + (uint64_t)(2048 >> 4) * ks, kIdescPV, (j | ks) != 0);
+                // a chunk's boxes of page_rows (packed: all 128) keys; a lane looks one up
+                const int pr = paged ? a.page_rows : kPC, nbox = kPC / pr;
+                const CUtensorMap* map = kv ? &a.mv : &a.mk;
+                // (row in the page or packed row, page * Hkv + kv-head or kv-head); z < 0: not loaded
+                auto look_up = [&](int j, int& y, int& z) {
+                    const int pos = (c0 + j) * kPC + lane * pr;
+                    y = 0;
+                    z = -1;
+                    if (lane >= nbox || j >= cmax || pos >= keys) return;
+                    if (!paged) {
+                        y = sq.r0 + pos;
+                        z = g;
+                        return;
+                    }
+                    const int page = p.block_table[(long)b * p.max_pages + pos / p.page_size];
+                    if (page >= 0 && page < p.num_pages) {
+                        y = pos % p.page_size;
+                        z = page * p.Hkv + g;
+                    } else {
+                        set_status(p.status, MEDUSA_STATUS_BAD_PAGE);
+                    }
                 };
-                wait(&kv_full[s], (i / ST) & 1);
-                const int part = c0 + j - (pos0 + 1) / kPC;
-                if (part >= 0) wait(&v_clean[part], 0);
+                int next_y, next_z, issued = 0;
+                look_up(0, next_y, next_z);
+                for (int j = 0; j < cmax; ++j) {
+                    const int y = next_y, z = next_z, i = 2 * j + kv, s = i % ST;
+                    look_up(j + 1, next_y, next_z);  // one chunk ahead: in flight during this chunk's wait
+                    const unsigned loads = __ballot_sync(kFull, z >= 0);
+                    if (i >= ST && !__all_sync(kFull, mbar_wait(&kv_empty[s], ((i / ST) - 1) & 1, wait_ns))) {
+                        if (lane == 0) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
+                        break;
+                    }
+                    if (lead) mbar_arrive_expect_tx(&kv_full[s], (uint32_t)(__popc(loads) * NSUB * pr * 128));
+                    ++issued;
+                    for (int x = 0; x < nbox; ++x) {
+                        const int by = __shfl_sync(kFull, y, x), bz = __shfl_sync(kFull, z, x);
+                        if (bz < 0) continue;
+                        if (lead) {
 #pragma unroll
-                for (int x = 0; x < kPParts; ++x) {
-                    constexpr int kSteps = kPC / 16 / kPParts;
-                    wait(&p_full[tile * kPParts + x], j & 1);
+                            for (int sub = 0; sub < NSUB; ++sub)
+                                tma_load_3d(sKV + s * kTile + sub * kSub + x * pr * 128, map, sub * 64,
+                                            paged ? by : bz, paged ? bz : by, &kv_full[s]);
+                        }
+                        __syncwarp();
+                    }
+                }
+                // drain: no copy may still be landing when the CTA exits
+                if (kv == 0 && cnt0 > 0) mbar_wait(&q_full[0], 0);
+                if (kv == 0 && cnt1 > 0) mbar_wait(&q_full[1], 0);
+                for (int j = max(0, issued - (ST + 1) / 2); j < issued; ++j) {
+                    const int i = 2 * j + kv;  // (a stage that the other producer has used since had landed)
+                    if (i + ST >= 2 * issued) mbar_wait(&kv_full[i % ST], (i / ST) & 1);
+                }
+            }
+        } else if (warp < 3) {
+            // ---------------- MMA issuer of a tile ----------------
+            // A warp per tile, so that the waits of one do not hold up the other's
+            // products.  The whole warp runs the loop, so that descriptors and
+            // addresses stay in uniform registers; one elected lane issues.
+            const int tile = warp - 1;
+            const int n = __shfl_sync(kFull, tile ? cnt1 : cnt0, 0), other = __shfl_sync(kFull, tile ? cnt0 : cnt1, 0);
+            if (n > 0) {
+                const bool lead = elect_one();
+                const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+                // a stage is free after one arrival for each tile (two of the only one that uses it)
+                auto release = [&](int s, int j) {
+                    tc_commit(&kv_empty[s]);
+                    if (j >= other) tc_commit(&kv_empty[s]);
+                };
+                const uint64_t qd = sw128_kmajor_desc(smem_addr(sQ) + tile * kQTile);
+                const uint64_t kd = sw128_kmajor_desc(smem_addr(sKV));
+                const uint64_t vd = p_mnmajor_desc(smem_addr(sKV), kSub);
+                const uint32_t t_s = tm + tile * kPC, t_o = tm + 256 + tile * 128;
+                auto issue_qk = [&](int j) {
+                    const int i = 2 * j, s = i % ST;
+                    wait(&kv_full[s], (i / ST) & 1);
                     tc_fence_after();
                     if (lead) {
 #pragma unroll
-                        for (int ks = 0; ks < kSteps; ++ks) pv(x * kSteps + ks);
-                        tc_commit(&o_full[tile]);
+                        for (int sub = 0; sub < NSUB; ++sub)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                tc_mma_bf16(t_s, qd + (uint64_t)((sub * kQSub) >> 4) + 2 * ks,
+                                            kd + (uint64_t)((s * kTile + sub * kSub) >> 4) + 2 * ks, kIdescQK,
+                                            (sub | ks) != 0);
+                        // completes after this tile's products so far: its last PV too
+                        tc_commit(&s_full[tile]);
+                        release(s, j);
                     }
                     __syncwarp();
+                };
+                wait(&q_full[tile], 0);
+                issue_qk(0);
+                for (int j = 0; j < n; ++j) {
+                    const int i = 2 * j + 1, s = i % ST;
+                    const uint64_t bd = vd + (uint64_t)((s * kTile) >> 4);
+                    auto pv = [&](int ks) {  // 16 keys: 8 columns of P, two 1024-byte groups of V
+                        tc_mma_bf16_ts(t_o, t_s + ks * 8, bd + (uint64_t)(2048 >> 4) * ks, kIdescPV, (j | ks) != 0);
+                    };
+                    wait(&kv_full[s], (i / ST) & 1);
+                    const int part = c0 + j - (pos0 + 1) / kPC;
+                    if (part >= 0) wait(&v_clean[part], 0);
+#pragma unroll
+                    for (int x = 0; x < kPParts; ++x) {
+                        constexpr int kSteps = kPC / 16 / kPParts;
+                        wait(&p_full[tile * kPParts + x], j & 1);
+                        tc_fence_after();
+                        if (lead) {
+#pragma unroll
+                            for (int ks = 0; ks < kSteps; ++ks) pv(x * kSteps + ks);
+                            tc_commit(&o_full[tile]);
+                        }
+                        __syncwarp();
+                    }
+                    if (lead) {
+                        release(s, j);
+                        if (j + 1 == n) tc_commit(&o_last[tile]);
+                    }
+                    __syncwarp();
+                    if (j + 1 < n) issue_qk(j + 1);  // over P: the products run in issue order
                 }
-                if (lead) {
-                    release(s, j);
-                    if (j + 1 == n) tc_commit(&o_last[tile]);
-                }
-                __syncwarp();
-                if (j + 1 < n) issue_qk(j + 1);  // over P: the products run in issue order
+                if (!ok) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
+                mbar_wait(&o_last[tile], 0);  // every product issued has finished writing TMEM
             }
-            if (!ok) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
-            mbar_wait(&o_last[tile], 0);  // every product issued has finished writing TMEM
         }
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------- softmax ----------------
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
         bool pending = false;  // the last weights were large: m is to be raised by `rise`
         float rise = 0.f;
         auto raise = [&](int done) {  // after `done` parts of PV products
-            const float alpha = pending ? p_exp2(-rise) : 1.f;
+            const float alpha = pending ? exp2_sfu(-rise) : 1.f;
             if (pending) m += rise;
             pending = false;
             l *= alpha;
@@ -403,7 +410,8 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                         continue;
                     }
                     const uint4 w = *at;
-                    const uint32_t b0 = nonfinite2(w.x), b1 = nonfinite2(w.y), b2 = nonfinite2(w.z), b3 = nonfinite2(w.w);
+                    const uint32_t b0 = nonfinite2(w.x), b1 = nonfinite2(w.y);
+                    const uint32_t b2 = nonfinite2(w.z), b3 = nonfinite2(w.w);
                     if (b0 | b1 | b2 | b3) {
                         *at = make_uint4(clear2(w.x, b0), clear2(w.y, b1), clear2(w.z, b2), clear2(w.w, b3));
                         s_tile[5] = 1;
@@ -457,10 +465,10 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                                                    __uint_as_float(raw[k >> 4][(k & 15) + 1])), sc2, mu2);
                         float p0, p1;
                         split2(t, p0, p1);
-                        p0 = p_exp2(p0);
-                        p1 = p_exp2(p1);
+                        p0 = exp2_sfu(p0);
+                        p1 = exp2_sfu(p1);
                         s2[e & 1] = add2(s2[e & 1], f2(p0, p1));
-                        pk[e >> 4][e & 15] = p_pack(p0, p1);
+                        pk[e >> 4][e & 15] = pack_bf16(p0, p1);
                     }
                     float s0, s1;
                     split2(add2(s2[0], s2[1]), s0, s1);
@@ -470,7 +478,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                     const float mx = row_max();
                     pending = mx > m;
                     rise = mx - m;
-                    if (pending) sum *= p_exp2(-rise);
+                    if (pending) sum *= exp2_sfu(-rise);
                     raise(j * kPParts + x);
                 }
                 l += part;
@@ -559,7 +567,8 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                     const int r = x * kRows + lane / kRowVecs, c = lane % kRowVecs, q = (warp & 3) * 32 + r;
                     const int t = div_by(q, a.div_G);
                     if (t < T && tile * T + t < ntok)
-                        *reinterpret_cast<uint4*>(base + (row0 + (long)(t * p.Hq + q - t * G)) * row_bytes + off + c * 16) =
+                        *reinterpret_cast<uint4*>(base + (row0 + (long)(t * p.Hq + q - t * G)) * row_bytes + off +
+                                                  c * 16) =
                             *reinterpret_cast<const uint4*>(stage + r * (2 * D) + ((c ^ r) & (kRowVecs - 1)) * 16);
                 }
                 __syncwarp();
@@ -578,9 +587,10 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
             } else {
 #pragma unroll
                 for (int x = 0; x < kRowVecs; ++x)
-                    put(x, make_uint4(p_pack(o[8 * x] * inv, o[8 * x + 1] * inv), p_pack(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
-                                      p_pack(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
-                                      p_pack(o[8 * x + 6] * inv, o[8 * x + 7] * inv)));
+                    put(x, make_uint4(pack_bf16(o[8 * x] * inv, o[8 * x + 1] * inv),
+                                      pack_bf16(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
+                                      pack_bf16(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
+                                      pack_bf16(o[8 * x + 6] * inv, o[8 * x + 7] * inv)));
                 store((uint8_t*)p.out, D * 2, 0);
             }
         }
@@ -596,7 +606,8 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
 
 template <int D>
 constexpr size_t prompt_tc_smem() {
-    return (size_t)(2 * kPM + p_stages<D>() * kPC) * D * 2 + (2 + 2 * p_stages<D>() + 7 + 2 * kPParts + kParts) * 8 + 32;
+    const int bars = 2 + 2 * p_stages<D>() + 7 + 2 * kPParts + kParts;
+    return (size_t)(2 * kPM + p_stages<D>() * kPC) * D * 2 + bars * 8 + 32;
 }
 static_assert(prompt_tc_smem<128>() <= 232448 && prompt_tc_smem<64>() <= 232448, "shared memory of a CTA");
 

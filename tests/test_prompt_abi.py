@@ -34,7 +34,7 @@ PLAN = dict(prefix_len=FAKE, new_len=FAKE, B=2, room=0, table=FAKE, max_pages=4,
     (dict(owned_out=NUL), INV), (dict(free=NUL), INV), (dict(count=NUL), INV), (dict(count_out=NUL), INV),
     (dict(row=NUL), INV), (dict(slots=NUL), INV), (dict(slots=ODD), INV), (dict(B=0), INV), (dict(room=-1), INV),
     (dict(max_pages=0), INV), (dict(page=0), INV), (dict(num=0), INV), (dict(max_tokens=0), INV),
-    (dict(max_pages=1 << 20, page=1 << 12), INV), (dict(B=8193), UNS)])
+    (dict(max_pages=1 << 20, page=1 << 12), INV), (dict(max_tokens=(1 << 30) + 1), INV), (dict(B=8193), UNS)])
 def test_plan_refuses(lib, kw, code):
     assert lib.kv_page_plan(*{**PLAN, **kw}.values()) == code
     assert b"kv_page_plan" in lib.medusa_last_error()
@@ -47,8 +47,8 @@ APPEND = dict(k=FAKE, v=FAKE, ks=1024, vs=1024, slots=FAKE, N=3, kp=FAKE, vp=FAK
 @pytest.mark.parametrize("kw,code", [
     (dict(k=NUL), INV), (dict(v=NUL), INV), (dict(slots=NUL), INV), (dict(kp=NUL), INV), (dict(vp=NUL), INV),
     (dict(k=ODD), INV), (dict(vp=ODD), INV), (dict(ks=1023), INV), (dict(vs=1028), INV), (dict(ks=-1024), INV),
-    (dict(N=-1), INV), (dict(page=0), INV), (dict(num=0), INV), (dict(Hkv=0), INV), (dict(D=96), UNS),
-    (dict(dt=2), UNS)])
+    (dict(N=-1), INV), (dict(page=0), INV), (dict(num=0), INV), (dict(Hkv=0), INV), (dict(N=1 << 28), INV),
+    (dict(page=1 << 16, num=1 << 16), INV), (dict(D=96), UNS), (dict(dt=2), UNS)])
 def test_append_refuses(lib, kw, code):
     assert lib.kv_append_paged(*{**APPEND, **kw}.values()) == code
     assert b"kv_append_paged" in lib.medusa_last_error()
@@ -78,7 +78,7 @@ CHUNK = dict(q=FAKE, qs=4096, kp=FAKE, vp=FAKE, table=FAKE, max_pages=4, page=16
 @pytest.mark.parametrize("kw,code", COMMON + [
     (dict(kp=NUL), INV), (dict(vp=ODD), INV), (dict(table=NUL), INV), (dict(prefix=NUL), INV),
     (dict(max_pages=0), INV), (dict(page=0), INV), (dict(num=0), INV), (dict(max_prefix=65), INV),
-    (dict(max_new=-1), INV)])
+    (dict(max_new=-1), INV), (dict(num=1 << 28), INV)])
 def test_chunk_refuses(lib, kw, code):
     assert lib.chunk_attention_paged(*{**CHUNK, **kw}.values()) == code
     assert b"chunk_attention_paged" in lib.medusa_last_error()
