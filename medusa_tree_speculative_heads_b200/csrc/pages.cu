@@ -125,7 +125,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_page_plan_kernel(const PagePl
         const bool served = fits && (grow == 0 || i_grow <= avail);
         if (fits && !served) bad |= MEDUSA_STATUS_CACHE_OVERFLOW;
         (void)block_scan(served ? grow : 0, s_warp, t_used);
-        if (b < a.B) s_off[b] = served ? (int)(i_grow - grow) : -1;
+        // (what refused sequences before it would have taken may pass 32 bits; a
+        // sequence served behind them takes nothing)
+        if (b < a.B) s_off[b] = served ? (int)min(i_grow - grow, 0x7fffffffL) : -1;
         grow0 += t_grow;
         used += t_used;
     }

@@ -85,6 +85,19 @@ def test_plan_refuses_what_does_not_fit_and_serves_the_rest():
     assert got["slot_map"].tolist()[:65] == [-1] * 65
 
 
+def test_plan_serves_what_takes_nothing_behind_refused_growth_past_32_bits():
+    """Five sequences that would take 2^29 - 1 pages each are refused; the
+    sixth needs no page and gets its slot."""
+    mp = 2 ** 29
+    table = torch.empty((6, mp), dtype=torch.int32, device="cuda")
+    table[5, 0] = 3
+    out = api.kv_page_plan(_ints([mp - 1] * 5 + [0]), _ints([0] * 5 + [1]), table, _ints([0] * 5 + [1]),
+                           _ints([0, 1, 2, 4]), _ints([4]), 1, 2)
+    assert out["status"].item() == B.STATUS_CACHE_OVERFLOW
+    assert out["slot_map"].tolist() == [3, -1] and out["row_start"].tolist() == [0] * 6 + [1]
+    assert out["owned"].tolist() == [0] * 5 + [1] and out["free_count"].item() == 4
+
+
 def test_plan_reports_values_out_of_range():
     def status(prefix=(0,), new=(1,), owned=(0,), stack=(1, 0), table=((-1, -1),), max_tokens=8):
         return _run(list(prefix), list(new), list(owned), [list(r) for r in table], list(stack), 4, 16, 0, max_tokens)
