@@ -671,7 +671,7 @@ int kv_append_paged(const void* k, const void* v, int64_t k_stride, int64_t v_st
  *   starts mean nothing.
  * scale: softmax scale; <= 0 means 1/sqrt(D)
  * out [N, Hq, D] dtype dt (contiguous); lse [N, Hq] f32, nullable: natural
- *   log-sum-exp of the scaled scores
+ *   log-sum-exp of the scaled scores; neither overlaps an input
  * K/V of tokens that a row does not see never reach its output, whatever
  * they hold (NaN and infinities included).
  * fp32 computes in fp32 throughout; bf16 multiplies bf16 weights (fp32
