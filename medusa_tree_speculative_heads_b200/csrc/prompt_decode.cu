@@ -268,6 +268,13 @@ __global__ void __launch_bounds__(kDThreads, kDCtasPerSm) decode_kernel(const __
         };
         int y = 0, z = -1, qrow = 0, qhead = 0;
         bool first = true;  // the chunk is its pair's first in this run
+        // A slot may be filled again when its readers are done and its last copy has
+        // landed.  The one implies the other, unless a wait expired and they passed
+        // the slot over: its barrier then must not be armed for a second copy.
+        auto free_slot = [&](uint64_t* empty, uint64_t* full, int parity) {
+            return __all_sync(kFull, mbar_wait(empty, parity, a.wait_ns)) &&
+                   __all_sync(kFull, mbar_wait(full, parity, a.wait_ns));
+        };
         if (more) look_up(y, z);
         while (more && ok) {
             const int s = it % ST, cy = y, cz = z;
@@ -283,7 +290,7 @@ __global__ void __launch_bounds__(kDThreads, kDCtasPerSm) decode_kernel(const __
             if (more) look_up(y, z);
             if (cfirst) {
                 const int qs = seg & 1;
-                if (seg >= 2 && !__all_sync(kFull, mbar_wait(&sm.q_empty[qs], ((seg >> 1) - 1) & 1, a.wait_ns))) {
+                if (seg >= 2 && !free_slot(&sm.q_empty[qs], &sm.q_full[qs], ((seg >> 1) - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -297,7 +304,7 @@ __global__ void __launch_bounds__(kDThreads, kDCtasPerSm) decode_kernel(const __
                 ++seg;
             }
             const unsigned loads = __ballot_sync(kFull, cz >= 0);
-            if (it >= ST && !__all_sync(kFull, mbar_wait(&sm.empty[s], ((it / ST) - 1) & 1, a.wait_ns))) {
+            if (it >= ST && !free_slot(&sm.empty[s], &sm.full[s], ((it / ST) - 1) & 1)) {
                 ok = false;
                 break;
             }

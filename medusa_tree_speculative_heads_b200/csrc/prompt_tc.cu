@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
     uint64_t* v_clean = o_last + 2;    // [kParts] V of the chunks that some row sees in part is cleared
     uint64_t* stagger = v_clean + kParts;  // tile 0's first softmax is done
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stagger + 1);
-    volatile int* s_tile = reinterpret_cast<volatile int*>(tmem_slot + 1);  // b, t, r0, n, p, dirty
+    volatile int* s_tile = reinterpret_cast<volatile int*>(tmem_slot + 1);  // b, t, r0, n, p, dirty, chunks of K and V issued
 
     const PromptArgs& p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -265,7 +265,12 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                     const int y = next_y, z = next_z, i = 2 * j + kv, s = i % ST;
                     look_up(j + 1, next_y, next_z);  // one chunk ahead: in flight during this chunk's wait
                     const unsigned loads = __ballot_sync(kFull, z >= 0);
-                    if (i >= ST && !__all_sync(kFull, mbar_wait(&kv_empty[s], ((i / ST) - 1) & 1, wait_ns))) {
+                    // The stage's last copy has landed when its readers are done, unless a wait
+                    // expired and they passed it over: a barrier then must not be armed
+                    // for a second copy on top of the first.
+                    const int last = ((i / ST) - 1) & 1;
+                    if (i >= ST && !(__all_sync(kFull, mbar_wait(&kv_empty[s], last, wait_ns)) &&
+                                     __all_sync(kFull, mbar_wait(&kv_full[s], last, wait_ns)))) {
                         if (lane == 0) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
                         break;
                     }
@@ -286,9 +291,12 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                 // drain: no copy may still be landing when the CTA exits
                 if (kv == 0 && cnt0 > 0) mbar_wait(&q_full[0], 0);
                 if (kv == 0 && cnt1 > 0) mbar_wait(&q_full[1], 0);
-                for (int j = max(0, issued - (ST + 1) / 2); j < issued; ++j) {
-                    const int i = 2 * j + kv;  // (a stage that the other producer has used since had landed)
-                    if (i + ST >= 2 * issued) mbar_wait(&kv_full[i % ST], (i / ST) & 1);
+                if (lane == 0) s_tile[6 + kv] = issued;
+                asm volatile("bar.sync 1, 64;" ::: "memory");  // the two producers
+                const int others = s_tile[7 - kv];
+                for (int j = max(0, issued - ST); j < issued; ++j) {
+                    const int i = 2 * j + kv, next = i + ST;  // (a stage that was used again had landed)
+                    if (next >> 1 >= ((next & 1) == kv ? issued : others)) mbar_wait(&kv_full[i % ST], (i / ST) & 1);
                 }
             }
         } else if (warp < 3) {
@@ -607,7 +615,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
 template <int D>
 constexpr size_t prompt_tc_smem() {
     const int bars = 2 + 2 * p_stages<D>() + 7 + 2 * kPParts + kParts;
-    return (size_t)(2 * kPM + p_stages<D>() * kPC) * D * 2 + bars * 8 + 32;
+    return (size_t)(2 * kPM + p_stages<D>() * kPC) * D * 2 + bars * 8 + 48;
 }
 static_assert(prompt_tc_smem<128>() <= 232448 && prompt_tc_smem<64>() <= 232448, "shared memory of a CTA");
 

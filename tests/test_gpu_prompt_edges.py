@@ -151,3 +151,35 @@ def test_broadcast_rows_are_refused():
     with pytest.raises(B.MedusaError):
         api.kv_append_paged(wide, k, torch.arange(4, device="cuda"), *(torch.zeros((1, 2, 16, 64), dtype=BF16,
                                                                                   device="cuda"),) * 2)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,prefix", [([700], 0), ([2000, 3, 900], 0), ([64, 200], 3000), ([1, 1, 1], 3000)])
+def test_expired_waits_end_every_call(D, lens, prefix):
+    """With every wait giving up at once a call ends with the timeout reported,
+    however often; its producers and consumers run at their own pace then."""
+    g = _gen(61)
+    Hq, Hkv, page, total = 8, 2, 16, [prefix + n for n in lens]
+    k, v = (_rand((sum(total), Hkv, D), g, BF16) for _ in range(2))
+    kp, vp, table = _paged(k, v, total, page, g)
+    row, kr = _rows(lens), _rows(total)
+    q = _rand((row[-1], Hq, D), g, BF16)
+
+    def call():
+        if prefix:
+            return api.chunk_attention_paged(q, kp, vp, table, _ints(row), _ints([prefix] * len(lens)),
+                                             max_new=max(lens), max_prefix=prefix)
+        return api.prompt_attention(q, k, v, _ints(row))
+
+    B.set_wait_limit(1)
+    try:
+        bad = [call() for _ in range(20)]
+        torch.cuda.synchronize()
+    finally:
+        B.set_wait_limit(0)
+    assert all(x["status"].item() & B.STATUS_TIMEOUT for x in bad)
+    good = call()
+    assert good["status"].item() == 0
+    for b, n in enumerate(lens):
+        at = slice(row[b], row[b + 1])
+        R.check(good["out"][at], None, BF16, D, R.attention(q[at], k[kr[b]:kr[b + 1]], v[kr[b]:kr[b + 1]], prefix))
