@@ -225,10 +225,8 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
             if (cmax > 0) {
                 const bool lead = elect_one();
                 const int kv = warp == 3;
-                if (kv == 0) {
-#pragma unroll
-                    for (int tile = 0; tile < 2; ++tile) {
-                        if ((tile == 0 ? cnt0 : cnt1) == 0 || !lead) continue;
+                auto load_q = [&](int tile) {
+                    if ((tile == 0 ? cnt0 : cnt1) > 0 && lead) {
                         mbar_arrive_expect_tx(&q_full[tile], (uint32_t)(T * G * 128 * NSUB));
 #pragma unroll
                         for (int sub = 0; sub < NSUB; ++sub)
@@ -236,7 +234,12 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                                         sq.r0 + tok0 + tile * T, &q_full[tile]);
                     }
                     __syncwarp();
-                }
+                };
+                // Copies are served in the order of their issue, and filling Q and the
+                // ring takes some 3400 cycles: the Q and K of the first product come
+                // first, and V waits for them.
+                if (kv == 0) load_q(0);
+                else asm volatile("bar.sync 2, 64;" ::: "memory");
                 // a chunk's boxes of page_rows (packed: all 128) keys; a lane looks one up
                 const int pr = paged ? a.page_rows : kPC, nbox = kPC / pr;
                 const CUtensorMap* map = kv ? &a.mv : &a.mk;
@@ -286,6 +289,10 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                                             paged ? by : bz, paged ? bz : by, &kv_full[s]);
                         }
                         __syncwarp();
+                    }
+                    if (j == 0 && kv == 0) {
+                        load_q(1);
+                        asm volatile("bar.arrive 2, 64;" ::: "memory");
                     }
                 }
                 // drain: no copy may still be landing when the CTA exits
