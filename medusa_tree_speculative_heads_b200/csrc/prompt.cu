@@ -291,6 +291,7 @@ struct PromptPlan {
     bool tc;
     int M, T, splits;
     long tiles;
+    bool table;  // the tiles are found by a launch of their own
 };
 
 PromptPlan prompt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hkv, int page_size, medusa_dtype dt) {
@@ -317,6 +318,9 @@ PromptPlan prompt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hk
     if (s > most) s = most;
     if (s > kMaxSplits) s = kMaxSplits;
     p.splits = s < 1 ? 1 : (int)s;
+    // A CTA of the tensor-core kernel takes some 2 us to find its tile among several
+    // sequences, a launch that finds them all some 3 us
+    p.table = p.tc && B > 1 && p.splits == 1 && p.tiles * Hkv > 2L * num_sms();
     return p;
 }
 
@@ -324,7 +328,7 @@ template <typename E, int D>
 cudaError_t prompt_dispatch(const PromptArgs& a, cudaStream_t st) {
     const PromptPlan p = prompt_plan(a.B, a.N, a.max_new, a.max_prefix, a.Hq, a.Hkv, a.page_size, a.dt);
     const SplitBuf buf = split_buf(a.ws, (long)a.N * a.Hq, D, p.splits);
-    cudaError_t e = p.tc ? prompt_tc_launch(a, p.tiles, p.splits, buf, st)
+    cudaError_t e = p.tc ? prompt_tc_launch(a, p.tiles, p.splits, buf, p.table ? a.ws : nullptr, st)
                   : p.M == 16 ? simt_launch<E, D, 1>(a, p.tiles, p.T, p.splits, buf, st)
                               : simt_launch<E, D, 4>(a, p.tiles, p.T, p.splits, buf, st);
     if (e != cudaSuccess || p.splits == 1) return e;
@@ -358,7 +362,10 @@ size_t prompt_workspace_size(int B, int N, int max_new, int max_prefix, int Hq, 
     const long part = rows < most ? rows : most;
     const size_t split = align256((size_t)part * D * 4) + align256((size_t)part * 4);
     const size_t few = decode_supported(B, 1, Hq, Hkv, page_size, dt) ? decode_workspace_size(D) : 0;
-    return few > split ? few : split;
+    const bool tc = prompt_tc_supported(page_size, dt);
+    const size_t table = tc ? prompt_table_bytes(N / prompt_tc_tokens(Hq / Hkv) + (B < N ? B : N)) : 0;
+    const size_t most2 = few > split ? few : split;
+    return most2 > table ? most2 : table;
 }
 
 cudaError_t prompt_launch(const PromptArgs& a, cudaStream_t st) {

@@ -209,7 +209,9 @@ inline SplitBuf split_buf(void* ws, long rows, int D, int splits) {
 bool prompt_tc_supported(int page_size, medusa_dtype dt);
 int prompt_tc_tokens(int G);
 int prompt_tc_chunk();
-cudaError_t prompt_tc_launch(const PromptArgs& a, long tiles, int splits, const SplitBuf& buf, cudaStream_t st);
+cudaError_t prompt_tc_launch(const PromptArgs& a, long tiles, int splits, const SplitBuf& buf, void* table,
+                             cudaStream_t st);
+size_t prompt_table_bytes(long tiles);
 // few rows per (sequence, kv-head) over a paged cache (bf16)
 bool decode_supported(int B, int max_new, int Hq, int Hkv, int page_size, medusa_dtype dt);
 size_t decode_workspace_size(int D);

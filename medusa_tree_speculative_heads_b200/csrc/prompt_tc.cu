@@ -74,6 +74,7 @@ struct PromptTcArgs {
     SplitBuf buf;
     int G, T, page_rows;
     FastDiv div_2T, div_G;
+    const int4* table;  // the grid's tiles, two entries of four each (NULL: every CTA finds its own)
     float scale_log2;
     uint64_t wait_ns;
 };
@@ -113,6 +114,18 @@ __device__ __forceinline__ uint64_t p_mnmajor_desc(uint32_t addr, uint32_t lbo) 
     return d;
 }
 
+// The tiles of a grid, a warp each: {b, t, r0, n}, {p}.
+__global__ void __launch_bounds__(256) prompt_table_kernel(const __grid_constant__ PromptTcArgs a, int4* table,
+                                                           int tiles) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int idx = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (idx >= tiles) return;
+    const PromptTile t = prompt_tile(a.p, 2 * a.T, a.div_2T, idx);
+    if ((threadIdx.x & 31) != 0) return;
+    table[2 * idx] = make_int4(t.b, t.t, t.s.r0, t.s.n);
+    table[2 * idx + 1] = make_int4(t.s.p, 0, 0, 0);
+}
+
 template <int D, bool kTestWaits>
 __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_constant__ PromptTcArgs a) {
     const uint64_t wait_ns = kTestWaits ? a.wait_ns : kWaitLimitNs;
@@ -149,15 +162,17 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
         return;
     }
     if (warp == 0) {
-        const PromptTile t = prompt_tile(p, 2 * T, a.div_2T, blockIdx.x / p.Hkv);
-        if (lane == 0) {
-            s_tile[0] = t.b;
-            s_tile[1] = t.t;
-            s_tile[2] = t.s.r0;
-            s_tile[3] = t.s.n;
-            s_tile[4] = t.s.p;
-            s_tile[5] = 0;
+        if (!a.table) {
+            const PromptTile t = prompt_tile(p, 2 * T, a.div_2T, blockIdx.x / p.Hkv);
+            if (lane == 0) {
+                s_tile[0] = t.b;
+                s_tile[1] = t.t;
+                s_tile[2] = t.s.r0;
+                s_tile[3] = t.s.n;
+                s_tile[4] = t.s.p;
+            }
         }
+        if (lane == 0) s_tile[5] = 0;
         if (blockIdx.x == 0 && split == 0)
             for (int b = lane; b < p.B; b += 32)
                 if (const int bad = prompt_seq(p, b).bad) set_status(p.status, bad);
@@ -182,15 +197,26 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
         mbar_init(stagger, 4);
         mbar_fence_init();
     }
+    int4 found;
+    int first;
+    if (a.table) {  // written by the launch before, which this one may have started under
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        found = __ldcg(a.table + 2 * (blockIdx.x / p.Hkv));
+        first = __ldcg(a.table + 2 * (blockIdx.x / p.Hkv) + 1).x;
+    }
     tc_fence_before();
     sync_block();
     tc_fence_after();
+    if (!a.table) {
+        found = make_int4(s_tile[0], s_tile[1], s_tile[2], s_tile[3]);
+        first = s_tile[4];
+    }
     const uint32_t tmem = *tmem_slot;
-    const int b = s_tile[0];
+    const int b = found.x;
     const struct {
         int r0, n, p;
-    } sq = {s_tile[2], s_tile[3], s_tile[4]};
-    const int tok0 = s_tile[1] * 2 * T;
+    } sq = {found.z, found.w, first};
+    const int tok0 = found.y * 2 * T;
     const int ntok = b < 0 ? 0 : min(2 * T, sq.n - tok0);
     const int pos0 = sq.p + tok0;                       // the first row's position
     const int keys = pos0 + ntok;                       // seen by the last row
@@ -635,7 +661,10 @@ bool prompt_tc_supported(int page_size, medusa_dtype dt) {
 int prompt_tc_tokens(int G) { return 2 * (kPM / G); }
 int prompt_tc_chunk() { return kPC; }
 
-cudaError_t prompt_tc_launch(const PromptArgs& x, long tiles, int splits, const SplitBuf& buf, cudaStream_t st) {
+size_t prompt_table_bytes(long tiles) { return (size_t)tiles * 2 * sizeof(int4); }
+
+cudaError_t prompt_tc_launch(const PromptArgs& x, long tiles, int splits, const SplitBuf& buf, void* table,
+                             cudaStream_t st) {
     PromptTcArgs a;
     const uint64_t D = x.D, Hq = x.Hq, Hkv = x.Hkv, N = x.N;
     a.G = x.Hq / x.Hkv;
@@ -672,8 +701,23 @@ cudaError_t prompt_tc_launch(const PromptArgs& x, long tiles, int splits, const 
     const size_t smem = x.D == 128 ? prompt_tc_smem<128>() : prompt_tc_smem<64>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)(tiles * x.Hkv), splits), kPW * 32, smem, st>>>(a);
-    return cudaGetLastError();
+    a.table = (const int4*)table;
+    if (table) {
+        prompt_table_kernel<<<(unsigned)((tiles + 7) / 8), 256, 0, st>>>(a, (int4*)table, (int)tiles);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * x.Hkv), splits);
+    cfg.blockDim = dim3(kPW * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = table ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace medusa
