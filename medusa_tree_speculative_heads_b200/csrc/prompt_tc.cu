@@ -38,11 +38,20 @@
 // exponentials, 1024 cycles of the SM's 16 per clock.  One tile alone takes
 // 3300 cycles a chunk (softmax 1650, products 1024, two hand-overs of some 200
 // to 300), both together 4300: each slows the other's exponentials and
-// products.  One prompt of 32768 tokens, 32/8 heads of 128: 7.9 to 8.3 ms, 1.06
-// to 1.12 PFLOP/s (7.05 ms, 1.25 PFLOP/s, before the clock drops under the
-// power cap); 2048 tokens 46.5 us, of which the prologue (tile lookup, the
-// first K) and the epilogue are some 6 us for each of the up to two CTAs of an
-// SM.
+// products.  One prompt of 32768 tokens, 32/8 heads of 128: 7.7 to 8.2 ms, 1.07
+// to 1.14 PFLOP/s (7.05 ms, 1.25 PFLOP/s, before the clock drops under the
+// power cap); 2048 tokens 45 us; 16 prompts of up to 4096, 240 us.
+//
+// What a CTA does once costs it some 9000 cycles beside 3700 per chunk: up to 5000
+// to its first S (launch, tile, and some 512 copied lines of 128 bytes for the Q
+// and K of the first product, served in the order of their issue, so they come
+// first), 4000 from its last product on (half of it 64 KB through the SM's write
+// path).  Finding its tile among several sequences costs 3000 cycles more; a
+// large grid gets its tiles from a launch of its own, which this one starts under.
+// Tried and slower: persistent CTAs that load across tiles (their loop over
+// chunks is 5 to 10% slower, one ring stage less costs another 2%), the first
+// copies issued before the block's first barrier (2%), an epilogue of rolled
+// loops (2%).
 //
 // The visible keys of a row are 0 .. its position, so only the chunks that
 // reach past the tile's first position need a mask.  In those, V elements
@@ -263,7 +272,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
                 };
                 // Copies are served in the order of their issue, and filling Q and the
                 // ring takes some 3400 cycles: the Q and K of the first product come
-                // first, and V waits for them.
+                // first, and V waits for them (2048 tokens 46.7 -> 45 us).
                 if (kv == 0) load_q(0);
                 else asm volatile("bar.sync 2, 64;" ::: "memory");
                 // a chunk's boxes of page_rows (packed: all 128) keys; a lane looks one up
