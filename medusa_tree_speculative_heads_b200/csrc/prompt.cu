@@ -318,10 +318,12 @@ PromptPlan prompt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hk
     if (s > most) s = most;
     if (s > kMaxSplits) s = kMaxSplits;
     p.splits = s < 1 ? 1 : (int)s;
-    // A CTA of the tensor-core kernel takes 3000 cycles to find its tile among several
-    // sequences, a launch that finds them all some 3 us: from two CTAs per SM on the
-    // launch pays (16 prompts of up to 4096 tokens, 10 CTAs per SM: 250 -> 240 us)
-    p.table = p.tc && B > 1 && p.splits == 1 && p.tiles * Hkv > 2L * num_sms();
+    // A CTA of the tensor-core kernel takes up to 3000 cycles to find its tile among
+    // several sequences, a launch that finds them all some 3 us.  Without and with it:
+    // 64 prompts of 64 tokens (3.5 CTAs per SM) 44.4 and 45.8 us, 8 of 1024 (7) 121.5
+    // and 121.6, 128 of 64 (7) 99 and 92, 16 of up to 4096 (10) 250 and 240, 40 of 512
+    // (17) 255 and 228.
+    p.table = p.tc && B > 1 && p.splits == 1 && p.tiles * Hkv > 4L * num_sms();
     return p;
 }
 
