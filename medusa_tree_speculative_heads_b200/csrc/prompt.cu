@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
     __shared__ int s_ok[kSimtKeys];  // the key exists (its page is valid)
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int g = blockIdx.x % a.Hkv, C = gridDim.y, split = blockIdx.y;
+    if (C > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge of splits
     if (tid < 32) {
         const PromptTile t = prompt_tile(a, T, div_T, blockIdx.x / a.Hkv);
         if (tid == 0) {
@@ -227,43 +228,51 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
     }
 }
 
-// Merge of the splits of each row, in split order; a warp per row.  A split
-// with no visible key has the log2-sum-exp -inf and no weight.
+// Merge of the splits of each row, in split order; a warp per row, whose lanes
+// read the splits' log2-sum-exps, two each, and then the columns.  A split with
+// no visible key has the log2-sum-exp -inf and no weight.  Latency-bound: the
+// launch starts under the splits', finds its rows and waits for them.
 template <typename E, int D>
 __global__ void __launch_bounds__(256) prompt_combine_kernel(const PromptArgs a, const SplitBuf buf, int C) {
+    static_assert(kMaxSplits <= 64, "two splits per lane");
     const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5), rows = (long)a.N * a.Hq;
     const int lane = threadIdx.x & 31;
-    if (row >= rows) return;
     const int t = (int)(row / a.Hq);
     // rows of no sequence (behind the last one, past max_new) are left alone
-    if (t < a.row_start[0] || t >= a.row_start[a.B]) return;
-    int lo = 0, hi = a.B - 1;  // the last sequence that starts at or before t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.row_start[mid] <= t) lo = mid;
-        else hi = mid - 1;
+    bool mine = row < rows && t >= a.row_start[0] && t < a.row_start[a.B];
+    if (mine) {
+        int lo = 0, hi = a.B - 1;  // the last sequence that starts at or before t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.row_start[mid] <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        const PromptSeq sq = prompt_seq(a, lo);
+        mine = t >= sq.r0 && t < sq.r0 + sq.n;
     }
-    const PromptSeq sq = prompt_seq(a, lo);
-    if (t < sq.r0 || t >= sq.r0 + sq.n) return;
-    float M = -INFINITY;
-    bool nan = false;
-    for (int s = 0; s < C; ++s) {
-        const float x = buf.lse2[(long)s * rows + row];
-        M = fmaxf(M, x);
-        nan |= x != x;
-    }
+    // every block waits for the splits, so this launch never ends before them
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!mine) return;
+    auto lse2 = [&](int s) { return s < C ? buf.lse2[(long)s * rows + row] : -INFINITY; };
+    const float x0 = lse2(lane), x1 = lse2(lane + 32);
+    const bool nan = __any_sync(kFull, x0 != x0 || x1 != x1);
+    float M = fmaxf(x0, x1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    const float mu = M == -INFINITY ? 0.f : M;
+    const float w0 = exp2f(x0 - mu), w1 = exp2f(x1 - mu);
     constexpr int PL = D / 32;
     float acc[PL], wsum = 0.f;
 #pragma unroll
     for (int e = 0; e < PL; ++e) acc[e] = 0.f;
-    const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
     for (int s = 0; s < C; ++s) {
-        const float w = exp2f(buf.lse2[(long)s * rows + row] - mu);
-        if (w == 0.f) continue;  // (a NaN weight is not skipped)
+        const float w = __shfl_sync(kFull, s < 32 ? w0 : w1, s & 31);
         const float* src = buf.o + ((long)s * rows + row) * D + lane * PL;
         wsum += w;
 #pragma unroll
-        for (int e = 0; e < PL; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+        for (int e = 0; e < PL; ++e)
+            acc[e] = w == 0.f ? acc[e] : fmaf(w, src[e], acc[e]);  // (a NaN weight is not skipped)
     }
     const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
     E* dst = (E*)a.out + row * D + lane * PL;
@@ -312,9 +321,10 @@ PromptPlan prompt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hk
     const int keys = p.tc ? prompt_tc_chunk() : kSimtKeys;
     const long chunks = ((long)max_prefix + max_new + keys - 1) / keys;
     // one CTA per SM (CUDA cores: two); a split keeps at least 8 of the tensor-core
-    // kernel's chunks (the merge launch costs about as much as 4 of them), or 2
+    // kernel's chunks (the merge launch costs about as much as 4 of them), on CUDA
+    // cores, where a chunk takes some 5 us, one
     long s = items > 0 ? (p.tc ? 1L : 2L) * num_sms() / items : 1;
-    const long most = chunks / (p.tc ? 8 : 2);
+    const long most = chunks / (p.tc ? 8 : 1);
     if (s > most) s = most;
     if (s > kMaxSplits) s = kMaxSplits;
     p.splits = s < 1 ? 1 : (int)s;
@@ -342,15 +352,19 @@ cudaError_t prompt_dispatch(const PromptArgs& a, cudaStream_t st) {
 
 cudaError_t prompt_combine_launch(const PromptArgs& a, const SplitBuf& buf, int splits, cudaStream_t st) {
     const long rows = (long)a.N * a.Hq;
-    const unsigned blocks = (unsigned)((rows + 7) / 8);
-    if (a.dt == MEDUSA_F32) {
-        if (a.D == 128) prompt_combine_kernel<float, 128><<<blocks, 256, 0, st>>>(a, buf, splits);
-        else prompt_combine_kernel<float, 64><<<blocks, 256, 0, st>>>(a, buf, splits);
-    } else {
-        if (a.D == 128) prompt_combine_kernel<__nv_bfloat16, 128><<<blocks, 256, 0, st>>>(a, buf, splits);
-        else prompt_combine_kernel<__nv_bfloat16, 64><<<blocks, 256, 0, st>>>(a, buf, splits);
-    }
-    return cudaGetLastError();
+    void (*kern)(PromptArgs, SplitBuf, int);
+    if (a.dt == MEDUSA_F32) kern = a.D == 128 ? prompt_combine_kernel<float, 128> : prompt_combine_kernel<float, 64>;
+    else kern = a.D == 128 ? prompt_combine_kernel<__nv_bfloat16, 128> : prompt_combine_kernel<__nv_bfloat16, 64>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, buf, splits);
 }
 
 size_t prompt_workspace_size(int B, int N, int max_new, int max_prefix, int Hq, int Hkv, int D, int page_size,

@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kPW * 32, 1) prompt_tc_kernel(const __grid_con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = blockIdx.x % p.Hkv, C = gridDim.y, split = blockIdx.y;
     const int T = a.T, G = a.G;
+    if (C > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge of splits
     if (smem_addr(smem) & 1023u) {  // never expected (uniform over the grid)
         if (threadIdx.x == 0) set_status(p.status, MEDUSA_STATUS_TIMEOUT);
         return;
