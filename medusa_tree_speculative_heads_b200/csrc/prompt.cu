@@ -25,7 +25,9 @@ constexpr int kMaxTileRows = 256;  // rows per CTA of the tensor-core kernel
 // j, then output columns 4 tx + 64 c of the same rows, so that a row's maximum
 // and sum stay within half a warp.  Tiles are fp32 in shared memory (rows
 // padded by 4 floats: 16-byte reads of consecutive rows fall on distinct
-// banks); P overlays K.  Bound by the FMA pipe and its shared-memory operands.
+// banks); P overlays K.  Bound by latency and by shared-memory reads, some 4 us a
+// chunk: three sequences of up to 149 tokens, 4 heads of 64: 11.6 us; 12 sequences
+// decoding over up to 312 cached tokens, one head of 128: 14.5 us.
 template <typename E, int D, int MI>
 __global__ void __launch_bounds__(kSimtThreads, 2)
     prompt_simt_kernel(const PromptArgs a, const SplitBuf buf, int T, FastDiv div_T) {
@@ -36,7 +38,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
     float* sV = sK + kSimtKeys * LD;
     float* sP = sK;  // K is read before P is written
     __shared__ PromptTile s_tile;
-    __shared__ int s_ok[kSimtKeys];  // the key exists (its page is valid)
+    __shared__ long s_row[2][kSimtKeys];  // where the keys of this and the next chunk are; < 0: nowhere
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int g = blockIdx.x % a.Hkv, C = gridDim.y, split = blockIdx.y;
     if (C > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge of splits
@@ -91,37 +93,54 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
     }
     const float scale2 = a.scale * 1.4426950408889634f;
     int bad = 0;
-    for (int ch = c0; ch < c1; ++ch) {
-        const int k0 = ch * kSimtKeys;
-        __syncthreads();  // P and V of the previous chunk are read
-        for (int e = tid; e < kSimtKeys * CV; e += kSimtThreads) {
-            const int r = e / CV, c = e % CV, key = k0 + r;
-            const E* ks = nullptr;
-            const E* vs = nullptr;
-            if (key < keys) {
-                if (a.block_table) {
-                    const int page = a.block_table[(long)b * a.max_pages + key / a.page_size];
-                    if (page >= 0 && page < a.num_pages) {
-                        const long at = (((long)page * a.Hkv + g) * a.page_size + key % a.page_size) * D;
-                        ks = (const E*)a.k + at;
-                        vs = (const E*)a.v + at;
-                    } else {
-                        bad = MEDUSA_STATUS_BAD_PAGE;
-                    }
-                } else {
-                    ks = (const E*)a.k + (long)(sq.r0 + key) * a.k_stride + g * D;
-                    vs = (const E*)a.v + (long)(sq.r0 + key) * a.v_stride + g * D;
-                }
-            }
-            if (ks) {
-                load_row(sK + r * LD, ks, c);
-                load_row(sV + r * LD, vs, c);
+    // A row of the pools or of packed K/V, by the thread of its key, a chunk ahead: the
+    // lookup and the loads that depend on it would wait one after the other.
+    const long k_stride = a.block_table ? D : a.k_stride, v_stride = a.block_table ? D : a.v_stride;
+    const E* const kb = (const E*)a.k + (a.block_table ? 0 : g * D);
+    const E* const vb = (const E*)a.v + (a.block_table ? 0 : g * D);
+    auto locate = [&](int ch) {
+        const int key = ch * kSimtKeys + tid;
+        if (tid >= kSimtKeys) return;
+        long row = -1;
+        if (ch < c1 && key < keys) {
+            if (a.block_table) {
+                const int page = a.block_table[(long)b * a.max_pages + key / a.page_size];
+                if (page >= 0 && page < a.num_pages) row = ((long)page * a.Hkv + g) * a.page_size + key % a.page_size;
+                else bad = MEDUSA_STATUS_BAD_PAGE;
             } else {
-                zero_row(sK + r * LD, c);
-                zero_row(sV + r * LD, c);
+                row = sq.r0 + key;
             }
-            if (c == 0) s_ok[r] = ks != nullptr;
         }
+        s_row[ch & 1][tid] = row;
+    };
+    locate(c0);
+    for (int ch = c0; ch < c1; ++ch) {
+        const int k0 = ch * kSimtKeys, nk = min(kSimtKeys, keys - k0);  // keys that some row sees
+        const long* at = s_row[ch & 1];
+        __syncthreads();  // P and V of the previous chunk are read
+        auto load = [&](float* dst, const E* src, long stride) {  // all of a thread's loads before its stores
+            constexpr int kEach = kSimtKeys * CV / kSimtThreads;
+            uint4 w[kEach];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int e = tid + i * kSimtThreads, r = e / CV, c = e % CV;
+                w[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (at[r] >= 0) w[i] = ld_nc(src + at[r] * stride + c * V4);
+            }
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                const int e = tid + i * kSimtThreads, r = e / CV, c = e % CV;
+                float f[V4];
+                Elt<E>::unpack(w[i], f);
+#pragma unroll
+                for (int x = 0; x < V4; x += 4)
+                    *reinterpret_cast<float4*>(dst + r * LD + c * V4 + x) =
+                        make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
+            }
+        };
+        load(sK, kb, k_stride);
+        load(sV, vb, v_stride);
+        locate(ch + 1);
         __syncthreads();
         float s[MI][4];
 #pragma unroll
@@ -134,11 +153,13 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
 #pragma unroll
             for (int i = 0; i < MI; ++i) qv[i] = *reinterpret_cast<const float4*>(sQ + (ty + 16 * i) * LD + d);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sK + (tx + 16 * j) * LD + d);
+            for (int j = 0; j < 4; ++j)
+                if (16 * j < nk) kv[j] = *reinterpret_cast<const float4*>(sK + (tx + 16 * j) * LD + d);
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
+                    if (16 * j >= nk) continue;
                     s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
                     s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
                     s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
@@ -152,7 +173,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = tx + 16 * j;
-                s[i][j] = k0 + r <= pos[i] && s_ok[r] ? s[i][j] * scale2 : -INFINITY;
+                s[i][j] = k0 + r <= pos[i] && at[r] >= 0 ? s[i][j] * scale2 : -INFINITY;
                 mx = fmaxf(mx, s[i][j]);
             }
 #pragma unroll
@@ -176,7 +197,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2)
         }
         __syncthreads();
         const bool diag = k0 + kSimtKeys > sq.p + tok0 + 1;  // some row does not see some key
-        for (int k = 0; k < kSimtKeys; k += 4) {
+        for (int k = 0; k < nk; k += 4) {
             float4 pv[MI];
 #pragma unroll
             for (int i = 0; i < MI; ++i) pv[i] = *reinterpret_cast<const float4*>(sP + (ty + 16 * i) * LP + k);
@@ -309,7 +330,7 @@ PromptPlan prompt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hk
     p.tc = prompt_tc_supported(page_size, dt);
     // CUDA cores: the small tile for up to 16 rows per (sequence, kv-head),
     // decoding, and where the large one leaves SMs idle (three sequences of up to
-    // 149 tokens at 4 heads, 24 CTAs of 64 rows: 23.5 us; in tiles of 16: 14.8 us)
+    // 149 tokens at 4 heads, 24 CTAs of 64 rows: 23.5 us; in tiles of 16: 14.8 us then)
     p.M = p.tc ? kMaxTileRows : 64;
     if (!p.tc && G <= 16 &&
         ((long)max_new * G <= 16 || prompt_tiles(B, N, max_new, 64 / G) * Hkv < num_sms()))
@@ -322,7 +343,7 @@ PromptPlan prompt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hk
     const long chunks = ((long)max_prefix + max_new + keys - 1) / keys;
     // one CTA per SM (CUDA cores: two); a split keeps at least 8 of the tensor-core
     // kernel's chunks (the merge launch costs about as much as 4 of them), on CUDA
-    // cores, where a chunk takes some 5 us, one
+    // cores, where a chunk takes some 4 us, one
     long s = items > 0 ? (p.tc ? 1L : 2L) * num_sms() / items : 1;
     const long most = chunks / (p.tc ? 8 : 1);
     if (s > most) s = most;
