@@ -183,3 +183,53 @@ def test_expired_waits_end_every_call(D, lens, prefix):
     for b, n in enumerate(lens):
         at = slice(row[b], row[b + 1])
         R.check(good["out"][at], None, BF16, D, R.attention(q[at], k[kr[b]:kr[b + 1]], v[kr[b]:kr[b + 1]], prefix))
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,lens,prefix", [
+    (F32, 8, 2, 128, [1, 1], 840),              # CUDA cores, split keys
+    (BF16, 8, 2, 128, [64], 4000),              # two tiles, split keys
+    (BF16, 32, 8, 128, [256] * 20, 0),          # a grid whose tiles are found first
+    (BF16, 8, 2, 64, [1, 2, 1], 2500)])         # few rows
+def test_replays_of_calls_of_two_launches(dtype, Hq, Hkv, D, lens, prefix):
+    """Captured twice in a row over the same buffers, replayed with other values
+    and with shorter sequences: bit for bit what the calls give by themselves."""
+    g = _gen(67)
+    page, row = 16, _rows(lens)
+    total = [prefix + n for n in lens]
+    k, v = (_rand((sum(total), Hkv, D), g, dtype) for _ in range(2))
+    kp, vp, table = _paged(k, v, total, page, g)
+    qs = [_rand((row[-1], Hq, D), g, dtype) for _ in range(2)]
+    q, rs, pre = qs[0].clone(), _ints(row), _ints([prefix] * len(lens))
+    step = api.PromptStep(B=len(lens), Hq=Hq, Hkv=Hkv, D=D, max_tokens=row[-1], dtype=dtype, page_size=page,
+                          max_pages=table.shape[1], num_pages=kp.shape[0], max_new=max(lens), max_prefix=prefix or 1)
+
+    def call():
+        if prefix:
+            step.chunk_attention(q, kp, vp, table, pre, row_start=rs)
+        else:
+            step.prompt_attention(q, k, v, row_start=rs)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+        first = step.out.clone()
+        call()
+    for values, shorter in ((qs[0], 0), (qs[1], 0), (qs[1], 1)):
+        q.copy_(values)
+        rs.copy_(_ints([min(r, row[-1] - shorter) for r in row]))
+        step.out.zero_()
+        call()
+        want = step.out.clone()
+        step.out.zero_()
+        first.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(step.out, want) and torch.equal(first, want)
+        assert step.status.item() == 0
+    for b, n in enumerate(lens[:2] if len(lens) > 2 else lens[:1]):
+        at, keys = slice(row[b], row[b + 1]), slice(_rows(total)[b], _rows(total)[b + 1])
+        ref = R.attention(q[at], k[keys], v[keys], prefix)
+        if row[b + 1] <= row[-1] - 1:
+            R.check(step.out[at], None, dtype, D, ref)
