@@ -15,9 +15,6 @@ namespace medusa {
 namespace {
 
 constexpr int kSimtThreads = 256;
-constexpr int kSimtKeys = 64;  // keys per chunk
-constexpr int kMaxSplits = 64;
-constexpr int kMaxTileRows = 256;  // rows per CTA of the tensor-core kernel
 
 // One CTA takes M = 16 * MI rows (row = token * G + query head of the group)
 // of one (sequence, kv-head) and one split of its key chunks.  A 16 x 16 grid
@@ -316,51 +313,10 @@ cudaError_t simt_launch(const PromptArgs& a, long tiles, int T, int splits, cons
     return cudaGetLastError();
 }
 
-// The plan of a call: rows per tile, tokens per tile, key splits.
-struct PromptPlan {
-    bool tc;
-    int M, T, splits;
-    long tiles;
-    bool table;  // the tiles are found by a launch of their own
-};
-
-PromptPlan prompt_plan(int B, int N, int max_new, int max_prefix, int Hq, int Hkv, int page_size, medusa_dtype dt) {
-    PromptPlan p;
-    const int G = Hq / Hkv;
-    p.tc = prompt_tc_supported(page_size, dt);
-    // CUDA cores: the small tile for up to 16 rows per (sequence, kv-head),
-    // decoding, and where the large one leaves SMs idle (three sequences of up to
-    // 149 tokens at 4 heads, 24 CTAs of 64 rows: 23.5 us; in tiles of 16: 14.8 us then)
-    p.M = p.tc ? kMaxTileRows : 64;
-    if (!p.tc && G <= 16 &&
-        ((long)max_new * G <= 16 || prompt_tiles(B, N, max_new, 64 / G) * Hkv < num_sms()))
-        p.M = 16;
-    p.T = p.tc ? prompt_tc_tokens(G) : p.M / G;
-    p.tiles = prompt_tiles(B, N, max_new, p.T);
-    // (not fewer than the packed rows fill: the workspace bound counts on it)
-    const long items = (p.tiles > N / p.T ? p.tiles : N / p.T) * Hkv;
-    const int keys = p.tc ? prompt_tc_chunk() : kSimtKeys;
-    const long chunks = ((long)max_prefix + max_new + keys - 1) / keys;
-    // one CTA per SM (CUDA cores: two); a split keeps at least 8 of the tensor-core
-    // kernel's chunks (the merge launch costs about as much as 4 of them), on CUDA
-    // cores, where a chunk takes some 4 us, one
-    long s = items > 0 ? (p.tc ? 1L : 2L) * num_sms() / items : 1;
-    const long most = chunks / (p.tc ? 8 : 1);
-    if (s > most) s = most;
-    if (s > kMaxSplits) s = kMaxSplits;
-    p.splits = s < 1 ? 1 : (int)s;
-    // A CTA of the tensor-core kernel takes up to 3000 cycles to find its tile among
-    // several sequences, a launch that finds them all some 3 us.  Without and with it:
-    // 64 prompts of 64 tokens (3.5 CTAs per SM) 44.4 and 45.8 us, 8 of 1024 (7) 121.5
-    // and 121.6, 128 of 64 (7) 99 and 92, 16 of up to 4096 (10) 250 and 240, 40 of 512
-    // (17) 255 and 228.
-    p.table = p.tc && B > 1 && p.splits == 1 && p.tiles * Hkv > 4L * num_sms();
-    return p;
-}
-
 template <typename E, int D>
 cudaError_t prompt_dispatch(const PromptArgs& a, cudaStream_t st) {
-    const PromptPlan p = prompt_plan(a.B, a.N, a.max_new, a.max_prefix, a.Hq, a.Hkv, a.page_size, a.dt);
+    const PromptPlan p = prompt_plan(num_sms(), prompt_tc_supported(a.page_size, a.dt), a.B, a.N, a.max_new,
+                                     a.max_prefix, a.Hq, a.Hkv);
     const SplitBuf buf = split_buf(a.ws, (long)a.N * a.Hq, D, p.splits);
     cudaError_t e = p.tc ? prompt_tc_launch(a, p.tiles, p.splits, buf, p.table ? a.ws : nullptr, st)
                   : p.M == 16 ? simt_launch<E, D, 1>(a, p.tiles, p.T, p.splits, buf, st)
@@ -391,14 +347,10 @@ cudaError_t prompt_combine_launch(const PromptArgs& a, const SplitBuf& buf, int 
 size_t prompt_workspace_size(int B, int N, int max_new, int max_prefix, int Hq, int Hkv, int D, int page_size,
                              medusa_dtype dt) {
     (void)max_new;
-    // An upper bound that grows with N (a call with fewer rows may split its
-    // keys more): splits * tiles * Hkv is at most one CTA per SM of
-    // kMaxTileRows rows (CUDA cores: two of 64), so the partial rows are at
-    // most the rows of that many tiles, and at most kMaxSplits per row.
     (void)max_prefix;
-    const long most = (long)num_sms() * kMaxTileRows, rows = (long)N * Hq * kMaxSplits;
-    const long part = rows < most ? rows : most;
-    const size_t split = align256((size_t)part * D * 4) + align256((size_t)part * 4);
+    // A bound that grows with N (a call with fewer rows may split its keys more):
+    // the plan takes no more splits than split_rows has room for.
+    const size_t split = split_bytes(split_rows(num_sms(), N, Hq), D);
     const size_t few = decode_supported(B, 1, Hq, Hkv, page_size, dt) ? decode_workspace_size(D) : 0;
     // (a call whose keys are split has a small grid and no table)
     const bool tc = prompt_tc_supported(page_size, dt);

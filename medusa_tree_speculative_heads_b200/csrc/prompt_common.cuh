@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "prompt_plan.h"
 
 namespace medusa {
 
@@ -148,13 +149,6 @@ __device__ inline PromptTile prompt_tile(const PromptArgs& a, int T, FastDiv d, 
     return r;
 }
 
-// upper bound of the tiles of T tokens in a batch of at most N rows
-inline long prompt_tiles(int B, int N, int max_new, int T) {
-    const long per = (max_new + T - 1) / T;
-    const long packed = (long)N / T + (B < N ? B : N);
-    return per * B < packed ? per * B : packed;
-}
-
 // 2^x on the SFU (relative error about 2^-22; 2^-inf = 0)
 __device__ __forceinline__ float exp2_sfu(float x) {
     float y;
@@ -188,27 +182,21 @@ __device__ __forceinline__ uint32_t clear2(uint32_t w, uint32_t bad) {
     return w & ~((bad >> 15) * 0xffffu);
 }
 
-// Partial results of key splits in the workspace: normalised fp32 rows
-// [splits][N * Hq][D] and their log2-sum-exps [splits][N * Hq].
+// Partial results of key splits in the workspace.
 struct SplitBuf {
     float* o;
     float* lse2;
 };
-inline size_t split_bytes(long rows, int D, int splits) {
-    return splits > 1 ? align256((size_t)splits * rows * D * 4) + align256((size_t)splits * rows * 4) : 0;
-}
 inline SplitBuf split_buf(void* ws, long rows, int D, int splits) {
     SplitBuf s{nullptr, nullptr};
     if (splits > 1) {
         s.o = (float*)ws;
-        s.lse2 = (float*)((char*)ws + align256((size_t)splits * rows * D * 4));
+        s.lse2 = (float*)((char*)ws + split_lse_at(splits * rows, D));
     }
     return s;
 }
-// tensor-core kernel (bf16): tokens per CTA, keys per chunk, launch
+// tensor-core kernel (bf16)
 bool prompt_tc_supported(int page_size, medusa_dtype dt);
-int prompt_tc_tokens(int G);
-int prompt_tc_chunk();
 cudaError_t prompt_tc_launch(const PromptArgs& a, long tiles, int splits, const SplitBuf& buf, void* table,
                              cudaStream_t st);
 size_t prompt_table_bytes(long tiles);

@@ -67,11 +67,11 @@ namespace medusa {
 
 namespace {
 
-constexpr int kPW = 12;    // warps: 0 and 3 producers, 1 and 2 MMA, 4-11 softmax
-constexpr int kPM = 128;   // rows of a query tile
-constexpr int kParts = 3;  // most chunks that some row of a CTA sees in part: its 256 tokens and a first chunk
-constexpr int kPC = 128;   // keys per chunk
-constexpr int kPParts = 2; // parts of P
+constexpr int kPW = 12;             // warps: 0 and 3 producers, 1 and 2 MMA, 4-11 softmax
+constexpr int kPM = kPromptTcRows;  // rows of a query tile
+constexpr int kParts = 3;           // most chunks that some row of a CTA sees in part: its 256 tokens and a first chunk
+constexpr int kPC = kPromptTcKeys;  // keys per chunk
+constexpr int kPParts = 2;          // parts of P
 // K and V chunks share one ring (K0 V0 K1 V1 ...)
 template <int D> constexpr int p_stages() { return D == 128 ? 5 : 8; }
 
@@ -667,9 +667,6 @@ static_assert(prompt_tc_smem<128>() <= 232448 && prompt_tc_smem<64>() <= 232448,
 bool prompt_tc_supported(int page_size, medusa_dtype dt) {
     return dt == MEDUSA_BF16 && (page_size == 0 || attn_tc_page_ok(page_size));
 }
-
-int prompt_tc_tokens(int G) { return 2 * (kPM / G); }
-int prompt_tc_chunk() { return kPC; }
 
 size_t prompt_table_bytes(long tiles) { return (size_t)tiles * 2 * sizeof(int4); }
 
