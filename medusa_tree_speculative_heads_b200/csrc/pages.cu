@@ -66,17 +66,19 @@ __global__ void __launch_bounds__(kPlanThreads) kv_page_plan_kernel(const PagePl
         bad |= MEDUSA_STATUS_BAD_LENGTH;
         fc = fc < 0 ? 0 : a.num_pages;
     }
+    auto new_rows = [&](int b) {  // -1: ended; what is below that counts as no new row
+        const int n = a.new_len[b];
+        return n < -1 ? 0 : n;
+    };
     // pass 1: rows and released pages
     long rows0 = 0, rel0 = 0;
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
         long rows = 0, rel = 0;
         if (b < a.B) {
-            int n = a.new_len[b], own = a.owned[b];
-            if (n < -1) {
-                bad |= MEDUSA_STATUS_BAD_LENGTH;
-                n = 0;
-            }
+            const int n = new_rows(b);
+            int own = a.owned[b];
+            if (a.new_len[b] < -1) bad |= MEDUSA_STATUS_BAD_LENGTH;
             if (own < 0 || own > a.max_pages) {
                 bad |= MEDUSA_STATUS_BAD_LENGTH;
                 own = own < 0 ? 0 : a.max_pages;
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_page_plan_kernel(const PagePl
         long grow = 0;
         bool fits = false;
         if (b < a.B) {
-            const int n = a.new_len[b], p = a.prefix_len[b];
+            const int n = new_rows(b), p = a.prefix_len[b];
             if (n >= 0 && p < 0) bad |= MEDUSA_STATUS_BAD_PREFIX;
             if (n >= 0 && p >= 0) {
                 const long want = ((long)p + n + a.room + a.page_size - 1) / a.page_size;
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_page_plan_kernel(const PagePl
     auto valid = [&](int page) { return page >= 0 && page < a.num_pages; };
     // table entries, pushed pages and per-sequence outputs: a warp per sequence
     for (int b = rank + C * warp; b < a.B; b += C * (kPlanThreads / 32)) {
-        const int own = s_owned[b], off = s_off[b], n = a.new_len[b];
+        const int own = s_owned[b], off = s_off[b], n = new_rows(b);
         if (n == -1) {
             for (int i = lane; i < own; i += 32) {
                 const int page = a.block_table[(long)b * a.max_pages + i];
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_page_plan_kernel(const PagePl
                 if (s_rel[b] + i < nrel) a.free_list[fc + s_rel[b] + i] = page;
             }
         } else if (off >= 0) {
-            const int want = (int)(((long)a.prefix_len[b] + max(n, 0) + a.room + a.page_size - 1) / a.page_size);
+            const int want = (int)(((long)a.prefix_len[b] + n + a.room + a.page_size - 1) / a.page_size);
             for (int i = own + lane; i < want; i += 32) {
                 int page = stack_page(avail - 1 - (off + i - own));
                 if (!valid(page)) {

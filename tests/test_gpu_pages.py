@@ -199,3 +199,23 @@ def test_append_of_no_rows():
     k = torch.zeros((0, 2, 64), dtype=torch.bfloat16, device="cuda")
     out = api.kv_append_paged(k, k, torch.zeros(0, dtype=torch.int64, device="cuda"), kp, kp.clone())
     assert out["status"].item() == 0
+
+
+@pytest.mark.parametrize("room", [0, 40])
+def test_plan_takes_lengths_below_minus_one_as_zero(room):
+    """Reported, and otherwise planned like a sequence without new tokens: it
+    keeps its pages and gets those that its prefix and the room need."""
+    prefix, owned, stack = [20, 16, 5, 40, 0], [1, 1, 0, 3, 2], [0, 1, 2, 3, 9, 10, 11, 12, 13, 14]
+    table = [[4] + [-1] * 5, [5] + [-1] * 5, [-1] * 6, [6, 7, 8] + [-1] * 3, [15, 16] + [-1] * 4]
+    new, meant = [-2, 1, -7, -2 ** 31, -1], [0, 1, 0, 0, -1]
+    want = R.plan(prefix, meant, owned, table, stack, room, 16, 5)
+    got, tb, free = _run(prefix, new, owned, table, stack, 17, 16, room, 5)
+    assert not want[-1]
+    assert got["status"].item() == B.STATUS_BAD_LENGTH
+    _check(got, tb, free, want, len(stack), 16)
+    # where it does not fit, or its prefix is out of range, that is reported too
+    got, tb, _ = _run([20], [-2], [0], [[-1] * 2], [0], 4, 16, room, 5)
+    assert got["status"].item() == B.STATUS_BAD_LENGTH | B.STATUS_CACHE_OVERFLOW
+    assert got["owned"].tolist() == [0] and tb == [[-1] * 2] and got["free_count"].item() == 1
+    got, _, _ = _run([-3], [-2], [0], [[-1] * 2], [0], 4, 16, room, 5)
+    assert got["status"].item() == B.STATUS_BAD_LENGTH | B.STATUS_BAD_PREFIX
