@@ -50,14 +50,6 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs& a, int b) {
 // of runs of kWeightKeys keys that its last token sees.
 constexpr int kWeightKeys = 128;
 
-// exact x / T for 0 <= x < 2^31, 1 <= T <= 256: m = ceil(2^40 / T), whose excess
-// over 2^40 / T (below 1) moves x * m / 2^40 by less than 2^-9 < 1 / T
-struct FastDiv {
-    uint64_t m;
-};
-inline FastDiv fast_div(int T) { return FastDiv{((1ull << 40) + T - 1) / T}; }
-__device__ __forceinline__ int div_by(int x, FastDiv d) { return (int)(((uint64_t)(uint32_t)x * d.m) >> 40); }
-
 // Tiles of a sequence with at most w runs of kWeightKeys.
 __device__ __forceinline__ int tiles_upto(int n, int p, int T, FastDiv d, int w) {
     const int room = w * kWeightKeys - p;  // (keys stay below 2^30 + 2^30)

@@ -1,9 +1,17 @@
 // Launch arithmetic of the prompt and chunk attention kernels: tiles, key
-// splits and what they take of the workspace.  Host only and without CUDA, so
-// that it is checked on a CPU for any number of SMs.
+// splits and what they take of the workspace, and the division that finds a
+// tile.  Builds without CUDA, so that it is checked on a CPU for any number of
+// SMs.
 #pragma once
 
 #include <stddef.h>
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define MEDUSA_HD __host__ __device__ __forceinline__
+#else
+#define MEDUSA_HD inline
+#endif
 
 namespace medusa {
 
@@ -14,6 +22,21 @@ constexpr int kMaxSplits = 64;
 
 // tokens per CTA of the tensor-core kernel
 inline int prompt_tc_tokens(int G) { return 2 * (kPromptTcRows / G); }
+
+// Exact x / T for 0 <= x < 2^31, 1 <= T <= 256, as x * m >> s: with 2^c the power
+// of two at or above T, s = 31 + c and m = ceil(2^s / T) (below 2^32: T > 2^(c-1)),
+// the excess of m * T over 2^s is below T <= 2^c, so it moves the quotient by less
+// than x / 2^31 * 1 / T < 1 / T.
+struct FastDiv {
+    uint32_t m;
+    int s;
+};
+inline FastDiv fast_div(int T) {
+    int c = 0;
+    while ((1 << c) < T) ++c;
+    return FastDiv{(uint32_t)(((1ull << (31 + c)) + T - 1) / T), 31 + c};
+}
+MEDUSA_HD int div_by(int x, FastDiv d) { return (int)((uint64_t)(uint32_t)x * d.m >> d.s); }
 
 // upper bound of the tiles of T tokens in a batch of at most N rows
 inline long prompt_tiles(int B, int N, int max_new, int T) {
