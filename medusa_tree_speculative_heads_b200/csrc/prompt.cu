@@ -22,9 +22,10 @@ constexpr int kSimtThreads = 256;
 // j, then output columns 4 tx + 64 c of the same rows, so that a row's maximum
 // and sum stay within half a warp.  Tiles are fp32 in shared memory (rows
 // padded by 4 floats: 16-byte reads of consecutive rows fall on distinct
-// banks); P overlays K.  Bound by latency and by shared-memory reads, some 4 us a
-// chunk: three sequences of up to 149 tokens, 4 heads of 64: 11.6 us; 12 sequences
-// decoding over up to 312 cached tokens, one head of 128: 14.5 us.
+// banks); P overlays K.  Bound by latency and by shared-memory reads: a chunk
+// takes 6.4 us at 64 columns and 12.8 at 128 (16 rows, up to two CTAs per SM; 64
+// rows: 11 and 19).  Three sequences of up to 149 tokens, 4 heads of 64: 11.6 us; 12
+// sequences decoding over up to 312 cached tokens, one head of 128: 14.5 us.
 template <typename E, int D, int MI>
 __global__ void __launch_bounds__(kSimtThreads, 2)
     prompt_simt_kernel(const PromptArgs a, const SplitBuf buf, int T, FastDiv div_T) {

@@ -84,7 +84,7 @@ inline PromptPlan prompt_plan(int sms, bool tc, int B, int N, int max_new, int m
     const long chunks = ((long)max_prefix + max_new + keys - 1) / keys;
     // one CTA per SM (CUDA cores: two); a split keeps at least 8 of the tensor-core
     // kernel's chunks (the merge launch costs about as much as 4 of them), on CUDA
-    // cores, where a chunk takes some 4 us, one
+    // cores, where a chunk takes 6 to 19 us, one
     long s = items > 0 ? (p.tc ? 1L : 2L) * sms / items : 1;
     const long most = chunks / (p.tc ? 8 : 1);
     if (s > most) s = most;

@@ -38,9 +38,10 @@
 // exponentials, 1024 cycles of the SM's 16 per clock.  One tile alone takes
 // 3300 cycles a chunk (softmax 1650, products 1024, two hand-overs of some 200
 // to 300), both together 4300: each slows the other's exponentials and
-// products.  One prompt of 32768 tokens, 32/8 heads of 128: 7.7 to 8.2 ms, 1.07
-// to 1.14 PFLOP/s (7.05 ms, 1.25 PFLOP/s, before the clock drops under the
-// power cap); 2048 tokens 45 us; 16 prompts of up to 4096, 240 us.
+// products.  One prompt of 32768 tokens, 32/8 heads of 128: 7.7 to 8.4 ms, 1.05
+// to 1.15 PFLOP/s (6.84 ms, 1.29 PFLOP/s, after some seconds of idling, before the
+// clock drops under the power cap); 2048 tokens 46 us; 16 prompts of up to 4096,
+// 240 us.
 //
 // What a CTA does once costs it some 9000 cycles beside 3700 per chunk: up to 5000
 // to its first S (launch, tile, and some 512 copied lines of 128 bytes for the Q
